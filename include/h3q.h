@@ -240,6 +240,75 @@ h3q_status h3q_attention_int8(const void* q, const void* k, const void* v, int64
                               cudaStream_t stream);
 
 /*
+ * 8-bit floating-point linear layers with one scale per block of 128. The pages
+ * name online fp8 weights and activations for the same DiT (vllm-omni issue,
+ * MiniMax-H3 progress table; cloud-worker research findings); the format is the
+ * public block-scaled one: e4m3 codes, fp32 scales, activations in blocks of
+ * 1 x 128 along K, weights in blocks of 128 x 128. No rotation.
+ *   a = max|x| over the block; s = 0 where a = 0, else max(RN(a / 448), 2^-126);
+ *   q = e4m3_rne(RN(x * RN(1 / s))) (0 where s = 0). The last block of a row (and
+ *   the last block row of a weight) takes what remains.
+ * Layouts: codes [rows, K] bytes; activation scales sx [ceil(K / 128), M] fp32 (the
+ * scales of consecutive tokens are neighbours); weight scales sw [ceil(N / 128),
+ * ceil(K / 128)] fp32. Scales need not come from these quantizers: any finite fp32
+ * value is applied as it is.
+ * A NaN makes its block NaN, an infinity its own element, and with it the outputs
+ * that depend on them.
+ * K % 16 == 0, K >= 16; M (N) == 0 is a no-op; all pointers 16-byte aligned.
+ */
+h3q_status h3q_fp8_quantize(const void* x, int x_dtype, int64_t M, int64_t K, uint8_t* xq, float* sx,
+                            cudaStream_t stream);
+h3q_status h3q_fp8_prepare_weight(const void* w, int w_dtype, int64_t N, int64_t K, uint8_t* wq, float* sw,
+                                  cudaStream_t stream);
+
+/*
+ * acc[m][n] = sum over K blocks b of RN(sx[b][m] * sw[n / 128][b]) * sum_{k in b}
+ * xq[m][k] wq[n][k], the inner sums by the tensor cores in fp32, the outer one in
+ * fp32; v = acc + bias[n]; epilogues as h3q_linear_w8a8: y [M, N] bf16 = bf16(v), or
+ * with H3Q_EPI_SWIGLU (N = 2F, rows [0, F) the gate) y [M, F] = bf16(silu(v_gate) v_up).
+ * The result does not depend on timing: the same call gives the same bits.
+ *   N % 8 == 0 (SwiGLU: F % 128 == 0); K % 16 == 0; M >= 0.
+ */
+h3q_status h3q_linear_fp8(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq,
+                          const float* sw, int64_t N, const void* bias_bf16, int epilogue, void* y_bf16,
+                          cudaStream_t stream);
+
+/*
+ * The gate/up product whose output is the next product's input: h = silu(v_gate)
+ * v_up in fp32 (never rounded to bf16), quantized as h3q_fp8_quantize does:
+ * hq [M, F] codes, sh [F / 128, M] scales. N = 2F, F % 128 == 0.
+ */
+h3q_status h3q_linear_fp8_swiglu_quant(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq,
+                                       const float* sw, int64_t N, const void* bias_bf16, uint8_t* hq, float* sh,
+                                       cudaStream_t stream);
+
+/*
+ * RMS norm of every query and key head and the rotation of positions, in one pass
+ * (the step between the QKV projection and the attention; h3-rs README and the
+ * vllm-omni issue name it fused).
+ *   q: head h of token t is columns h D .. h D + D - 1 of row t of [S, ldq] bf16; k
+ *   likewise with Hk heads (Hk may differ from Hq; 0: no keys, k and k_out unused).
+ *   n = x * (1 / sqrt(mean(x^2) + eps)) * weight, fp32; q_weight, k_weight [D] bf16 or NULL.
+ *   Then a' = a c - b s, b' = b c + a s for the pairs (i, i + rot / 2), i < rot / 2
+ *   (interleaved == 0), or (2i, 2i + 1), of the first rot elements; the others are
+ *   only normalised. c, s: row `position` of cos, sin [P, rot / 2] fp32; positions
+ *   [S] int32, or NULL for positions 0, 1, ... (then P >= S). A position outside
+ *   [0, P) reads no table row and leaves its token's rotated elements NaN.
+ *   One rounding, to bf16 at the end. q_out, k_out [S, ld] may be q and k themselves
+ *   (same pointer and stride); other overlaps are not supported. Columns outside
+ *   the heads are neither read nor written.
+ *   16 <= D <= H3Q_QK_MAX_D, D % 16 == 0; rot % 16 == 0, 0 <= rot <= D (rot == 0: no
+ *   rotation, cos and sin unused); strides are multiples of 8; heads at most
+ *   H3Q_QK_MAX_HEADS; pointers 16-byte aligned (positions 4); 0 <= eps < inf.
+ */
+#define H3Q_QK_MAX_D 256
+#define H3Q_QK_MAX_HEADS 65536
+h3q_status h3q_qk_norm_rope(const void* q, const void* k, int64_t S, int64_t Hq, int64_t Hk, int64_t D, int64_t ldq,
+                            int64_t ldk, const void* q_weight, const void* k_weight, float eps, const float* cos,
+                            const float* sin, int64_t P, int64_t rot, int interleaved, const int32_t* positions,
+                            void* q_out, void* k_out, int64_t ldq_out, int64_t ldk_out, cudaStream_t stream);
+
+/*
  * The attention's input pass on its own (test hook and building block): qq, kq
  * int8 [H, S, 128], qs fp32 [H, S], ks fp32 [H, ceil(S / 128)] (one per block of
  * 128 keys), vt bf16 [H*128, S] (V^T per head).

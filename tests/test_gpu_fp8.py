@@ -1,0 +1,356 @@
+"""The fp8 block-scaled linear layer on the GPU against its definition in 64 bits.
+
+* Quantizers: bit-exact (every fp32 step of the definition is one rounding).
+* Products: the tensor cores add a block's 128 products in fp32 in an order of their own,
+  each of at most 128 additions off by at most one unit 2^-23 of the sum of magnitudes mag;
+  the scale product, its multiply-add per block and the few additions that join a split K
+  axis by 2^-24 each. So |acc - ref| <= e = (128 2^-23 + (KB + 18) 2^-24) mag, and the
+  bf16 result is off by half a step, 2^-8 of its value, more.
+* SwiGLU: |silu'| <= 1.1, so h is off by 1.1 e_g |u| + |silu(g)| e_u + 1.1 e_g e_u, and by
+  2^-17 |h| for the exponential and the reciprocal (|g| < 64 there); below, silu is under 2^-80.
+* Quantized h: a code stands for h within half a step, 2^-4 of the value or 2^-10 of the
+  scale, and the scale is the row block's largest |h| / 448 within that largest value's error.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+E4 = torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def h3q():
+    import w8a8_rotation_quantized_b200 as m
+    return m
+
+
+def _blocks(n):
+    return -(-n // 128)
+
+
+def _rne_e4m3(v):
+    """fp64 numpy -> nearest e4m3 value, ties to even, at most 448 in size."""
+    a = np.abs(v)
+    e = np.floor(np.log2(np.where((a > 0) & np.isfinite(a), a, 1.0)))
+    step = 2.0 ** (np.maximum(e, -6) - 3)
+    return np.clip(np.round(v / step) * step, -448.0, 448.0)
+
+
+def _scale(a):
+    a = np.asarray(a, np.float32)
+    with np.errstate(all="ignore"):
+        s = np.where(a == 0, np.float32(0), np.maximum(a / np.float32(448), np.float32(2.0 ** -126))).astype(np.float32)
+        inv = np.where(a == 0, np.float32(0), np.float32(1) / s).astype(np.float32)
+    return s, inv
+
+
+def _quantize_ref(x, rows):
+    """fp32 numpy [M, K] -> code values, scales [ceil(M / rows), KB] for blocks of rows x 128."""
+    M, K = x.shape
+    p = np.pad(x, ((0, -M % rows), (0, -K % 128)))
+    b = p.reshape(-1, rows, _blocks(K), 128)
+    s, inv = _scale(np.abs(b).max(axis=(1, 3)))
+    with np.errstate(all="ignore"):
+        t = (b * inv[:, None, :, None]).astype(np.float32)
+    codes = _rne_e4m3(t.astype(np.float64)).reshape(p.shape)[:M, :K]
+    return codes, s
+
+
+def _quantize(h3q, x):
+    M, K = x.shape
+    xq = torch.zeros(M, K, dtype=E4, device=x.device)
+    sx = torch.full((_blocks(K), M), -1.0, device=x.device)
+    h3q.h3q_fp8_quantize(x, xq, sx)
+    return xq, sx
+
+
+def _prepare(h3q, w):
+    N, K = w.shape
+    wq = torch.zeros(N, K, dtype=E4, device=w.device)
+    sw = torch.full((_blocks(N), _blocks(K)), -1.0, device=w.device)
+    h3q.h3q_fp8_prepare_weight(w, wq, sw)
+    return wq, sw
+
+
+def _input(M, K, seed, dev, dtype=torch.bfloat16):
+    g = torch.Generator().manual_seed(seed)
+    x = torch.randn(M, K, generator=g)
+    x[:, torch.randperm(K, generator=g)[: max(1, K // 100)]] *= 50
+    x *= 2.0 ** torch.randint(-12, 12, (M, 1), generator=g).float()
+    if M > 1:
+        x[M // 2] = 0
+    x[0, : min(K, 128)] = 0
+    return x.to(dtype).to(dev)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("M,K", [(1, 16), (1, 5376), (3, 128), (130, 144), (257, 1360), (64, 2064), (1000, 256)])
+def test_quantize_is_bit_exact(h3q, cuda_device, M, K, dtype):
+    x = _input(M, K, M + K, cuda_device, dtype)
+    xq, sx = _quantize(h3q, x)
+    codes, s = _quantize_ref(x.float().cpu().numpy(), 1)
+    assert np.array_equal(sx.cpu().numpy(), s.T)
+    assert np.array_equal(xq.float().cpu().numpy(), codes)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("N,K", [(8, 16), (128, 128), (136, 5376), (300, 1360), (1, 144)])
+def test_prepare_weight_is_bit_exact(h3q, cuda_device, N, K, dtype):
+    w = _input(N, K, N + K, cuda_device, dtype)
+    wq, sw = _prepare(h3q, w)
+    codes, s = _quantize_ref(w.float().cpu().numpy(), 128)
+    assert np.array_equal(sw.cpu().numpy(), s)
+    assert np.array_equal(wq.float().cpu().numpy(), codes)
+
+
+def test_quantize_extremes(h3q, cuda_device):
+    """The smallest and largest finite inputs, and what a NaN or an infinity reaches."""
+    x = torch.zeros(6, 256, dtype=torch.float32)
+    x[0, 3], x[0, 4] = 2.0 ** -149, -(2.0 ** -140)  # the scale stops at 2^-126: codes 0 or tiny
+    x[1] = torch.linspace(-3.4e38, 3.4e38, 256)  # the step overflows: infinities and NaN, equal in both
+    x[2, 5] = float("nan")
+    x[2, 6:200] = 1.0
+    x[3, 130] = float("inf")
+    x[3, :128] = 2.0
+    x[4, 7] = -0.0
+    x[5] = 2.0 ** -120
+    d = x.to(cuda_device)
+    xq, sx = _quantize(h3q, d)
+    v, s = xq.float().cpu().numpy(), sx.cpu().numpy().T
+    codes, want = _quantize_ref(x.numpy()[[0, 1, 4, 5]], 1)
+    assert np.array_equal(s[[0, 1, 4, 5]], want, equal_nan=True)
+    assert np.array_equal(v[[0, 1, 4, 5]], codes, equal_nan=True)
+    assert np.isnan(s[2, 0]) and np.isnan(v[2, :128]).all()
+    assert np.array_equal(v[2, 128:200], np.full(72, 448.0)) and s[2, 1] == np.float32(1) / np.float32(448)
+    assert np.isinf(s[3, 1]) and np.isnan(v[3, 130]) and not np.isnan(np.delete(v[3], 130)).any()
+    assert s[3, 0] == np.float32(2) / np.float32(448)
+    top = torch.linspace(-1, 1, 256)[None] * 3.4e38
+    xq, sx = _quantize(h3q, top.to(cuda_device))
+    codes, want = _quantize_ref(top.numpy(), 1)
+    assert np.isfinite(want).all() and np.array_equal(sx.cpu().numpy().T, want)
+    assert np.array_equal(xq.float().cpu().numpy(), codes)
+
+
+def _product_ref(xq, sx, wq, sw, bias):
+    """fp64 v [M, N] (bias added) and the sum of magnitudes of the products."""
+    x, w = xq.double(), wq.double()
+    v = torch.zeros(x.shape[0], w.shape[0], dtype=torch.float64, device=x.device)
+    mag = torch.zeros_like(v)
+    cols = sw.double().repeat_interleave(128, dim=0)[: w.shape[0]]
+    for b in range(_blocks(x.shape[1])):
+        k = slice(128 * b, 128 * b + 128)
+        f = sx[b].double()[:, None] * cols[:, b][None, :]
+        v += (x[:, k] @ w[:, k].T) * f
+        mag += (x[:, k].abs() @ w[:, k].abs().T) * f.abs()
+    if bias is not None:
+        v += bias.double()
+    return v, mag
+
+
+def _err(v, mag, K):
+    return (128 * 2.0 ** -23 + (_blocks(K) + 18) * 2.0 ** -24) * mag + 2.0 ** -24 * v.abs() + 2.0 ** -126
+
+
+def _swiglu_ref(v, e):
+    n = v.shape[1] // 2
+    g, u, eg, eu = v[:, :n], v[:, n:], e[:, :n], e[:, n:]
+    silu = g * torch.sigmoid(g)
+    h = silu * u
+    return h, 1.1 * eg * (u.abs() + eu) + silu.abs() * eu + 2.0 ** -17 * h.abs() + 2.0 ** -80 * u.abs()
+
+
+def _close(got, want, bound):
+    got = got.double()
+    assert torch.isfinite(got).all()
+    r = ((got - want).abs() / bound).max().item()
+    assert r <= 1, f"error is {r:.3g} of the bound"
+
+
+def _operands(h3q, M, K, N, seed, dev, with_bias):
+    xq, sx = _quantize(h3q, _input(M, K, seed, dev))
+    g = torch.Generator().manual_seed(seed + 1)
+    wq, sw = _prepare(h3q, (torch.randn(N, K, generator=g) * 0.02 * 2.0 ** torch.randint(-4, 4, (N, 1), generator=g)).to(dev))
+    bias = torch.randn(N, generator=g).bfloat16().to(dev) if with_bias else None
+    return xq, sx, wq, sw, bias
+
+
+SHAPES = [(1, 16, 8), (1, 128, 136), (2, 5376, 264), (3, 144, 1000), (7, 1360, 2056), (15, 512, 128), (16, 4096, 256),
+          (17, 272, 40), (31, 2064, 640), (33, 640, 3000), (64, 5376, 392), (65, 896, 1536), (127, 1024, 520),
+          (128, 14336, 256), (129, 256, 776), (200, 1920, 2048), (257, 128, 16), (300, 1360, 4352), (520, 2000, 1032),
+          (1025, 384, 2568), (4100, 144, 1288)]
+
+
+@pytest.mark.parametrize("M,K,N", SHAPES)
+def test_linear_within_bound(h3q, cuda_device, M, K, N):
+    xq, sx, wq, sw, bias = _operands(h3q, M, K, N, M + N, cuda_device, M % 2 == 1)
+    # rows behind the last are the caller's
+    y = torch.full((M + 3, N), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    h3q.h3q_linear_fp8(xq, sx, wq, sw, y[:M], bias=bias)
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+    assert (y[M:] == 7).all()
+    v, mag = _product_ref(xq, sx, wq, sw, bias)
+    e = _err(v, mag, K)
+    _close(y[:M], v, e + 2.0 ** -8 * (v.abs() + e))
+
+
+SWIGLU_SHAPES = [(1, 16, 128), (1, 5376, 640), (4, 144, 128), (16, 1360, 384), (40, 2064, 512), (64, 512, 1152),
+                 (100, 5376, 256), (128, 272, 896), (129, 640, 128), (300, 1360, 2176), (700, 256, 1280)]
+
+
+@pytest.mark.parametrize("M,K,F", SWIGLU_SHAPES)
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_swiglu_within_bound(h3q, cuda_device, M, K, F, with_bias):
+    xq, sx, wq, sw, bias = _operands(h3q, M, K, 2 * F, M + F, cuda_device, with_bias)
+    y = torch.full((M + 2, F), 7.0, dtype=torch.bfloat16, device=cuda_device)
+    h3q.h3q_linear_fp8(xq, sx, wq, sw, y[:M], bias=bias, epilogue=h3q.H3Q_EPI_SWIGLU)
+    hq = torch.full((M + 2, F), 3.0, device=cuda_device).to(E4)
+    sh = torch.full((F // 128 + 1, M), 5.0, device=cuda_device)
+    h3q.h3q_linear_fp8_swiglu_quant(xq, sx, wq, sw, hq[:M], sh[: F // 128], bias=bias)
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+    assert (y[M:] == 7).all() and (hq[M:].float() == 3).all() and (sh[F // 128 :] == 5).all()
+    v, mag = _product_ref(xq, sx, wq, sw, bias)
+    h, e = _swiglu_ref(v, _err(v, mag, K))
+    _close(y[:M], h, e + 2.0 ** -8 * (h.abs() + e) + 2.0 ** -133)
+    top = h.abs().view(M, -1, 128).amax(dim=2).T
+    e_top = e.view(M, -1, 128).amax(dim=2).T
+    got = sh[: F // 128]
+    _close(got, top / 448, e_top / 448 + 2.0 ** -23 * top + 2.0 ** -126)
+    back = hq[:M].double() * got.T.double().repeat_interleave(128, dim=1)
+    half_step = torch.maximum(2.0 ** -4 * (h.abs() + e), 2.0 ** -10 * got.T.double().repeat_interleave(128, dim=1))
+    _close(back, h, e + half_step * (1 + 2.0 ** -20) + 2.0 ** -126)
+
+
+def test_scales_of_any_value_are_applied(h3q, cuda_device):
+    """Negative, zero, huge and tiny scales, all codes: the product is what the operands say."""
+    M, K, N = 70, 400, 264
+    g = torch.Generator().manual_seed(4)
+    codes = torch.randint(0, 256, (M + N, K), generator=g, dtype=torch.uint8)
+    codes[(codes & 127) == 127] = 0  # the two NaN codes
+    codes = codes.to(cuda_device).view(E4)
+    xq, wq = codes[:M].contiguous(), codes[M:].contiguous()
+    sx = torch.randn(4, M, generator=g).to(cuda_device) * 2.0 ** torch.randint(-40, 40, (4, 1), generator=g).to(cuda_device)
+    sx[1, 5] = 0
+    sw = torch.randn(3, 4, generator=g).to(cuda_device)
+    sw[2, 0] = 0
+    y = torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device)
+    h3q.h3q_linear_fp8(xq, sx, wq, sw, y)
+    v, mag = _product_ref(xq, sx, wq, sw, None)
+    e = _err(v, mag, K)
+    _close(y, v, e + 2.0 ** -8 * (v.abs() + e))
+
+
+@pytest.mark.parametrize("M", [5, 300])
+def test_nan_and_infinity_stay_in_their_rows(h3q, cuda_device, M):
+    K, N = 512, 512
+    x = _input(M, K, 3, cuda_device)
+    clean = torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device)
+    wq, sw = _prepare(h3q, torch.randn(N, K, generator=torch.Generator().manual_seed(1)).to(cuda_device))
+    h3q.h3q_linear_fp8(*_quantize(h3q, x), wq, sw, clean)
+    x[1, 300], x[M - 1, 7] = float("nan"), float("inf")
+    y = torch.empty_like(clean)
+    h3q.h3q_linear_fp8(*_quantize(h3q, x), wq, sw, y)
+    assert torch.isnan(y[1]).all() and torch.isnan(y[M - 1]).all()
+    keep = [i for i in range(M) if i not in (1, M - 1)]
+    assert torch.equal(y[keep], clean[keep])
+    hq, sh = torch.empty(M, N // 2, dtype=E4, device=cuda_device), torch.empty(2, M, device=cuda_device)
+    h3q.h3q_linear_fp8_swiglu_quant(*_quantize(h3q, x), wq, sw, hq, sh)
+    assert torch.isnan(hq[1].float()).all() and torch.isnan(sh[:, M - 1]).all()
+    assert not torch.isnan(hq[keep].float()).any() and not torch.isnan(sh[:, keep]).any()
+
+
+@pytest.mark.parametrize("M,K,N", [(4, 5376, 512), (100, 2048, 768), (600, 1360, 1024)])
+def test_same_call_gives_the_same_bits(h3q, cuda_device, M, K, N):
+    xq, sx, wq, sw, bias = _operands(h3q, M, K, N, 9, cuda_device, True)
+    y = [torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device) for _ in range(6)]
+    for t in y:
+        h3q.h3q_linear_fp8(xq, sx, wq, sw, t, bias=bias)
+    assert all(torch.equal(t, y[0]) for t in y)
+
+
+def test_rows_do_not_depend_on_each_other(h3q, cuda_device):
+    """A row's result with its own batch size differs only by the order of the fp32 sums."""
+    K, N = 1360, 1032
+    xq, sx, wq, sw, bias = _operands(h3q, 400, K, N, 2, cuda_device, True)
+    v, mag = _product_ref(xq, sx, wq, sw, bias)
+    e = _err(v, mag, K)
+    for rows in (1, 20, 90, 400):
+        y = torch.empty(rows, N, dtype=torch.bfloat16, device=cuda_device)
+        h3q.h3q_linear_fp8(xq[:rows].contiguous(), sx[:, :rows].contiguous(), wq, sw, y, bias=bias)
+        _close(y, v[:rows], (e + 2.0 ** -8 * (v.abs() + e))[:rows])
+
+
+def test_two_streams_at_once(h3q, cuda_device):
+    sets = [_operands(h3q, M, 2048, 1024, M, cuda_device, False) for M in (8, 90, 700)]
+    want = [torch.empty(s[0].shape[0], 1024, dtype=torch.bfloat16, device=cuda_device) for s in sets]
+    for s, t in zip(sets, want):
+        h3q.h3q_linear_fp8(*s[:4], t)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = [[torch.empty_like(t) for t in want] for _ in streams]
+    for _ in range(5):
+        for st, outs in zip(streams, got):
+            for s, t in zip(sets, outs):
+                h3q.h3q_linear_fp8(*s[:4], t, stream=st)
+    torch.cuda.synchronize()
+    for outs in got:
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+@pytest.mark.parametrize("M", [1, 24, 300])
+def test_ffn_captured_and_replayed(h3q, cuda_device, M):
+    """quantize -> gate/up with quantized SwiGLU -> down, eager and as a replayed graph with new
+    inputs; and against the 64-bit product of the operands that each step was given."""
+    K, F = 1360, 640
+    dev = cuda_device
+    wq, sw = _prepare(h3q, torch.randn(2 * F, K, generator=torch.Generator().manual_seed(1)).to(dev) * 0.02)
+    dq, sd = _prepare(h3q, torch.randn(K, F, generator=torch.Generator().manual_seed(2)).to(dev) * 0.02)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+    xq, sx = torch.empty(M, K, dtype=E4, device=dev), torch.empty(_blocks(K), M, device=dev)
+    hq, sh = torch.empty(M, F, dtype=E4, device=dev), torch.empty(F // 128, M, device=dev)
+    y = torch.empty(M, K, dtype=torch.bfloat16, device=dev)
+
+    def ffn():
+        h3q.h3q_fp8_quantize(x, xq, sx)
+        h3q.h3q_linear_fp8_swiglu_quant(xq, sx, wq, sw, hq, sh)
+        h3q.h3q_linear_fp8(hq, sh, dq, sd, y)
+
+    x.copy_(_input(M, K, 1, dev))
+    ffn()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        ffn()
+    for seed in (2, 3):
+        x.copy_(_input(M, K, seed, dev))
+        ffn()
+        eager = [t.clone() for t in (xq.view(torch.uint8), sx, hq.view(torch.uint8), sh, y)]
+        for t in (xq, hq):
+            t.view(torch.uint8).zero_()
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((xq.view(torch.uint8), sx, hq.view(torch.uint8), sh, y), eager):
+            assert torch.equal(a, b)
+        v, mag = _product_ref(hq, sh, dq, sd, None)
+        e = _err(v, mag, F)
+        _close(y, v, e + 2.0 ** -8 * (v.abs() + e))
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+
+
+def test_binding_refuses_wrong_shapes(h3q, cuda_device):
+    xq, sx, wq, sw, bias = _operands(h3q, 5, 272, 264, 1, cuda_device, True)
+    y = torch.empty(5, 264, dtype=torch.bfloat16, device=cuda_device)
+    for args, kw in [((xq, sx.T.contiguous(), wq, sw, y), {}), ((xq, sx, wq[:, :256].contiguous(), sw, y), {}),
+                     ((xq, sx, wq, sw[:2], y), {}), ((xq, sx, wq, sw, y[:, :200]), {}), ((xq, sx, wq, sw, y[:4]), {}),
+                     ((xq, sx, wq, sw, y), {"bias": bias[:100]}), ((xq, sx, wq, sw, y.float()), {}),
+                     ((xq, sx, wq.t().contiguous().t(), sw, y), {})]:
+        with pytest.raises(ValueError):
+            h3q.h3q_linear_fp8(*args, **kw)
+    with pytest.raises(h3q.H3QError):  # 264 rows are not two halves of whole blocks
+        h3q.h3q_linear_fp8(xq, sx, wq, sw, y[:, :132].contiguous(), epilogue=h3q.H3Q_EPI_SWIGLU)
+    with pytest.raises(ValueError):
+        h3q.h3q_fp8_quantize(y, xq, sx)
+    empty = torch.empty(0, 272, dtype=E4, device=cuda_device)
+    h3q.h3q_linear_fp8(empty, torch.empty(3, 0, device=cuda_device), wq, sw, y[:0])

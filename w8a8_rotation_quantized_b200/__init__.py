@@ -44,6 +44,12 @@ _SIGS = {
     "h3q_attention_workspace_size": (_SZ, [_I64, _I64]),
     "h3q_attention_int8": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P, _I64, _P, _SZ, _P]),
     "h3q_attention_prep": (_INT, [_P, _P, _P, _I64, _I64, _I64, _P, _P, _P, _P, _P, _P]),
+    "h3q_fp8_quantize": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
+    "h3q_fp8_prepare_weight": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
+    "h3q_linear_fp8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P]),
+    "h3q_linear_fp8_swiglu_quant": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P]),
+    "h3q_qk_norm_rope": (_INT, [_P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _I64,
+                                _I64, _INT, _P, _P, _P, _I64, _I64, _P]),
     "h3q_gemm_s32": (_INT, [_P, _P, _I64, _I64, _I64, _P, _P]),
     "h3q_get_device_status": (_INT, [_P]),
     "h3q_set_wait_limit_ns": (None, [_U64]),
@@ -76,7 +82,7 @@ def _check(status: int, where: str) -> None:
 def _dtypes():
     import torch
     return {"bf16": torch.bfloat16, "f32": torch.float32, "i8": torch.int8, "u8": torch.uint8,
-            "i32": torch.int32}
+            "i32": torch.int32, "e4m3": torch.float8_e4m3fn}
 
 
 def _need(where: str, name: str, t, dtype: str, shape, device=None, dense: bool = True):
@@ -314,6 +320,123 @@ def h3q_attention_prep(q, k, v, H, qq, qs, kq, ks, vt, stream=None) -> None:
     _need(w, "vt", vt, "bf16", (H * 128, S), dev)
     _check(lib.h3q_attention_prep(_ptr(q), _ptr(k), _ptr(v), S, H, _ld(q), _ptr(qq), _ptr(qs), _ptr(kq), _ptr(ks),
                                   _ptr(vt), _stream(stream)), "h3q_attention_prep")
+
+
+def _on_device(name, fn, device, stream, *args):
+    """Calls fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
+    import torch
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, stream), name)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, stream), name)
+
+
+def _fp8_x_dtype(w, x):
+    """The dtype code of an fp8 quantizer's input [rows, K]."""
+    import torch
+    if x is not None and x.dtype == torch.bfloat16:
+        _need(w, "x", x, "bf16", (None, None))
+        return H3Q_DTYPE_BF16
+    _need(w, "x", x, "f32", (None, None))
+    return H3Q_DTYPE_F32
+
+
+def h3q_fp8_quantize(x, xq, sx, stream=None) -> None:
+    """x [M, K] bf16 or fp32 -> xq float8_e4m3fn [M, K], sx fp32 [ceil(K/128), M]: one scale
+    per token and 128 elements."""
+    w = "h3q_fp8_quantize"
+    dt = _fp8_x_dtype(w, x)
+    M, K = x.shape
+    dev = x.device
+    _need(w, "xq", xq, "e4m3", (M, K), dev)
+    _need(w, "sx", sx, "f32", ((K + 127) // 128, M), dev)
+    _on_device(w, lib.h3q_fp8_quantize, dev, stream, x.data_ptr(), dt, M, K, xq.data_ptr(), sx.data_ptr())
+
+
+def h3q_fp8_prepare_weight(w, wq, sw, stream=None) -> None:
+    """w [N, K] bf16 or fp32 -> wq float8_e4m3fn [N, K], sw fp32 [ceil(N/128), ceil(K/128)]:
+    one scale per 128 x 128 block."""
+    wh = "h3q_fp8_prepare_weight"
+    dt = _fp8_x_dtype(wh, w)
+    N, K = w.shape
+    dev = w.device
+    _need(wh, "wq", wq, "e4m3", (N, K), dev)
+    _need(wh, "sw", sw, "f32", ((N + 127) // 128, (K + 127) // 128), dev)
+    _on_device(wh, lib.h3q_fp8_prepare_weight, dev, stream, w.data_ptr(), dt, N, K, wq.data_ptr(), sw.data_ptr())
+
+
+def _fp8_operands(w, xq, sx, wq, sw, bias):
+    M, K = _need(w, "xq", xq, "e4m3", (None, None)).shape
+    dev = xq.device
+    N = _need(w, "wq", wq, "e4m3", (None, K), dev).shape[0]
+    KB = (K + 127) // 128
+    _need(w, "sx", sx, "f32", (KB, M), dev)
+    _need(w, "sw", sw, "f32", ((N + 127) // 128, KB), dev)
+    if bias is not None:
+        _need(w, "bias", bias, "bf16", (N,), dev)
+    return M, K, N, dev
+
+
+def h3q_linear_fp8(xq, sx, wq, sw, y, bias=None, epilogue=H3Q_EPI_NONE, stream=None) -> None:
+    """y bf16 [M, N] = block-scaled fp8 product of xq (sx) and wq (sw), + bias; SwiGLU
+    epilogue: y [M, N/2]."""
+    w = "h3q_linear_fp8"
+    M, K, N, dev = _fp8_operands(w, xq, sx, wq, sw, bias)
+    epilogue = int(epilogue)
+    _need(w, "y", y, "bf16", (M, N // 2 if epilogue == H3Q_EPI_SWIGLU else N), dev)
+    _on_device(w, lib.h3q_linear_fp8, dev, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(), sw.data_ptr(), N,
+               _ptr(bias), epilogue, y.data_ptr())
+
+
+def h3q_linear_fp8_swiglu_quant(xq, sx, wq, sw, hq, sh, bias=None, stream=None) -> None:
+    """hq float8_e4m3fn [M, F], sh fp32 [F/128, M] = quantized SwiGLU of the gate/up product
+    (wq [2F, K], gate rows first): the operands of the down projection."""
+    w = "h3q_linear_fp8_swiglu_quant"
+    M, K, N, dev = _fp8_operands(w, xq, sx, wq, sw, bias)
+    _need(w, "hq", hq, "e4m3", (M, N // 2), dev)
+    _need(w, "sh", sh, "f32", (N // 256, M), dev)
+    _on_device(w, lib.h3q_linear_fp8_swiglu_quant, dev, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(),
+               sw.data_ptr(), N, _ptr(bias), hq.data_ptr(), sh.data_ptr())
+
+
+H3Q_QK_MAX_D = 256
+
+
+def h3q_qk_norm_rope(q, k, Hq, Hk, D, cos, sin, q_out, k_out, q_weight=None, k_weight=None, positions=None,
+                     eps=1e-6, interleaved=False, stream=None) -> None:
+    """RMS norm of every head of q ([S, >= Hq D] bf16 view) and k ([S, >= Hk D], or None with
+    Hk = 0), then the rotation by row positions[t] (int32 [S]; None: row t) of cos, sin
+    (fp32 [P, rot/2]; None: no rotation). q_out, k_out: the same shapes, may be q and k."""
+    w = "h3q_qk_norm_rope"
+    S = _need(w, "q", q, "bf16", (None, None), dense=False).shape[0]
+    dev = q.device
+    views = [("q", q, Hq), ("q_out", q_out, Hq)]
+    if Hk:
+        views += [("k", k, Hk), ("k_out", k_out, Hk)]
+    for name, t, h in views:
+        _need(w, name, t, "bf16", (S, None), dev, dense=False)
+        if t.shape[1] < h * D:
+            raise ValueError(f"{w}: {name} must have at least {h * D} columns, got {t.shape[1]}")
+    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if t is not None:
+            _need(w, name, t, "bf16", (D,), dev)
+    P = half = 0
+    if cos is not None:
+        P, half = _need(w, "cos", cos, "f32", (None, None), dev).shape
+        _need(w, "sin", sin, "f32", (P, half), dev)
+    elif sin is not None:
+        raise ValueError(f"{w}: sin without cos")
+    if positions is not None:
+        _need(w, "positions", positions, "i32", (S,), dev)
+    # the stride of a single row means nothing (torch leaves any value there)
+    ldq, ldqo, ldk, ldko = [_ld(t) if S > 1 else h * D for _, t, h in views] + ([] if Hk else [0, 0])
+    _on_device(w, lib.h3q_qk_norm_rope, dev, stream, q.data_ptr(), _ptr(k) if Hk else None, S, Hq, Hk, D, ldq, ldk,
+               _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos), _ptr(sin), P, 2 * half, int(bool(interleaved)),
+               _ptr(positions), q_out.data_ptr(), _ptr(k_out) if Hk else None, ldqo, ldko)
 
 
 def h3q_gemm_s32(xq, wq, acc, stream=None) -> None:

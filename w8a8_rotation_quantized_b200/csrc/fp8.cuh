@@ -1,0 +1,527 @@
+// 8-bit floating-point linear layer with one scale per block of 128: e4m3 codes,
+// fp32 scales, activations in blocks of 1 x 128 (a token's 128 consecutive
+// elements), weights in blocks of 128 x 128.
+//
+//   quantize   a = max |x| over the block; s = 0 where a = 0, else
+//              max(RN(a / 448), 2^-126); q = e4m3_rne(RN(x * RN(1 / s))) (0 where
+//              s = 0). The bound 2^-126 keeps 1 / s finite.
+//   product    part_b = sum over the K block b of xq wq (tensor cores, fp32),
+//              acc = sum_b part_b * RN(sx[b][m] * sw[n / 128][b]), fused
+//              multiply-adds in fp32, b ascending; v = acc + bias;
+//              y = bf16(v), bf16(silu(v_gate) v_up), or the latter quantized
+//              again (1 x 128) straight from fp32.
+//
+// Layouts: xq [M, K], wq [N, K] row-major bytes; sx [ceil(K / 128), M] (the
+// product's threads hold one row each, so a K block's scales of consecutive rows
+// are one coalesced load); sw [ceil(N / 128), ceil(K / 128)].
+//
+// A NaN makes its block's scale and codes NaN, an infinity makes the scale
+// infinite and its own code NaN, so the outputs that depend on either are NaN.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include "gemm_sm100.cuh"
+#include "nvfp4.cuh"
+#include "ptx_sm100.cuh"
+
+namespace h3q {
+
+// max that returns NaN if either operand is NaN
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Two e4m3 codes (round to nearest even, saturating): lo in bits 0-7, hi in bits 8-15.
+__device__ __forceinline__ uint32_t f32x2_to_e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t f32x4_to_e4m3x4(float a, float b, float c, float d) {
+  return f32x2_to_e4m3x2(a, b) | (f32x2_to_e4m3x2(c, d) << 16);
+}
+
+// Scale of a block whose largest magnitude is a, and the factor that turns
+// elements into code values.
+__device__ __forceinline__ float fp8_scale(float a, float& inv) {
+  const float s = a == 0.0f ? 0.0f : max_nan(__fdiv_rn(a, 448.0f), 0x1p-126f);
+  inv = a == 0.0f ? 0.0f : __frcp_rn(s);
+  return s;
+}
+
+// ---------------------------------------------------------------- quantize
+// Eight consecutive elements as fp32.
+__device__ __forceinline__ void fp8_load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+__device__ __forceinline__ void fp8_load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+  v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+}
+
+__device__ __forceinline__ float fp8_absmax8(const float (&v)[8]) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max_nan(a, fabsf(v[i]));
+  return a;
+}
+
+__device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float inv) {
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) t[i] = __fmul_rn(v[i], inv);
+  return make_uint2(f32x4_to_e4m3x4(t[0], t[1], t[2], t[3]), f32x4_to_e4m3x4(t[4], t[5], t[6], t[7]));
+}
+
+// 1 x 128 blocks: sixteen lanes per block, eight elements each.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__ x, int64_t M, int K, int KB,
+                                                           uint8_t* __restrict__ codes, float* __restrict__ sx) {
+  const int64_t total = M * KB;
+  const int l = threadIdx.x & 15;
+  const int64_t first = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
+  const int64_t step = (int64_t(gridDim.x) * blockDim.x) >> 4;
+  const int64_t rounds = (total + step - 1) / step;
+  for (int64_t it = 0; it < rounds; ++it) {  // every lane runs every round: the shuffles need them all
+    const int64_t b = first + it * step;
+    const int64_t m = b / KB;
+    const int kb = static_cast<int>(b - m * KB);
+    const int col = kb * 128 + 8 * l;
+    const bool ok = b < total && col < K;
+    float v[8] = {};
+    if (ok) fp8_load8(x + m * K + col, v);
+    float a = fp8_absmax8(v);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+    float inv;
+    const float s = fp8_scale(a, inv);
+    if (ok) {
+      *reinterpret_cast<uint2*>(codes + m * K + col) = fp8_codes8(v, inv);
+      if (l == 0) sx[int64_t(kb) * M + m] = s;
+    }
+  }
+}
+
+// 128 x 128 blocks: one CTA of 256 threads per block; thread t holds the
+// 8-element chunks t + 256 n (row (t + 256 n) / 16), n = 0..7.
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_weight_kernel(const T* __restrict__ w, int64_t N, int K, int KB,
+                                                         uint8_t* __restrict__ codes, float* __restrict__ sw) {
+  __shared__ float warp_max[8];
+  const int64_t nb = blockIdx.x / KB;
+  const int kb = static_cast<int>(blockIdx.x - nb * KB);
+  const int col = kb * 128 + 8 * (threadIdx.x & 15);
+  float v[8][8];
+  float a = 0.0f;
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const int64_t row = nb * 128 + (threadIdx.x >> 4) + 16 * n;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[n][i] = 0.0f;
+    if (row < N && col < K) fp8_load8(w + row * K + col, v[n]);
+  }
+#pragma unroll
+  for (int n = 0; n < 8; ++n) a = max_nan(a, fp8_absmax8(v[n]));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+  if ((threadIdx.x & 31) == 0) warp_max[threadIdx.x >> 5] = a;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = max_nan(a, warp_max[i]);
+  float inv;
+  const float s = fp8_scale(a, inv);
+#pragma unroll
+  for (int n = 0; n < 8; ++n) {
+    const int64_t row = nb * 128 + (threadIdx.x >> 4) + 16 * n;
+    if (row < N && col < K) *reinterpret_cast<uint2*>(codes + row * K + col) = fp8_codes8(v[n], inv);
+  }
+  if (threadIdx.x == 0) sw[nb * KB + kb] = s;
+}
+
+// ---------------------------------------------------------------- product
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 x e4m3 -> fp32, CTA pair.
+__device__ __forceinline__ void mma_fp8_pair(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor for kind::f8f6f4: e4m3 A and B (format 0), fp32
+// accumulator, both operands K-major.
+__host__ __device__ constexpr uint32_t idesc_fp8(uint32_t M, uint32_t N) {
+  return (1u << 4)             // D format: f32
+         | ((N >> 3) << 17)    // N / 8
+         | ((M >> 4) << 24);   // M / 16
+}
+
+// tcgen05.wait::ld that the loaded registers depend on, so no use of them can be
+// scheduled before it.
+__device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]),
+                 "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]),
+                 "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// silu(g) = g / (1 + e^-g) from the hardware's 2^x and reciprocal approximations
+// (relative error about 2^-21 + |g| 2^-24, far below the bf16 or e4m3 rounding that
+// follows: e^-g is 2^x of a rounded product).
+// Below g = -88.7, e^-g overflows and the result is -0; silu is under 2^-121 there.
+__device__ __forceinline__ float silu_approx(float g) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.44269504f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, e)));
+  return __fmul_rn(g, r);
+}
+
+enum Fp8Epi : int { kF8BF16 = 0, kF8SwiGLU = 1, kF8SwiGLUQuant = 2 };
+
+constexpr int kF8Stages = 6;
+constexpr int kF8Threads = 384;  // producer, MMA, two idle warps, 8 promotion warps
+constexpr int kF8StageBytes = kAStage + kBStage;
+constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + 1024 /*align*/ + 256 /*barriers*/ + 2 * 2 * 128 * 4;
+// Register split: the launch's 168 per thread, moved from the first warpgroup to
+// the two that hold accumulators.
+constexpr uint32_t kF8RegsCtl = 40, kF8RegsPromote = 232, kF8RegsLaunch = 168;
+static_assert(128 * kF8RegsCtl + 256 * kF8RegsPromote <= kF8Threads * kF8RegsLaunch, "register split");
+
+struct Fp8Params {
+  int M, N, K;              // N: output columns (SwiGLU: F)
+  int KB;                   // K blocks: ceil(K / 128)
+  int num_m, num_n, num_tiles, group_m;
+  int b_row_up;             // SwiGLU: first up row of the weight (= F)
+  int last_nb;              // last row of sw
+  const float* sx;          // [KB, M]
+  const float* sw;          // [ceil(rows / 128), KB]
+  const __nv_bfloat16* bias;  // nullable
+  void* out;                // bf16 [M, N], or e4m3 codes
+  float* sh;                // SwiGLUQuant: [F / 128, M]
+  uint64_t wait_limit_ns;
+};
+
+// acc += part * f, 32 columns.
+__device__ __forceinline__ void f8_promote(float2 (&acc)[16], const uint32_t (&r)[32], float f) {
+  const float2 f2 = make_float2(f, f);
+#pragma unroll
+  for (int i = 0; i < 16; ++i)
+    acc[i] = __ffma2_rn(make_float2(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1])), f2, acc[i]);
+}
+
+// Adds eight bias values (or nothing) to acc[4 g .. 4 g + 3].
+__device__ __forceinline__ void f8_bias8(float2* acc, const __nv_bfloat16* bias) {
+  float b[8];
+  fp8_load8(bias, b);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[i] = __fadd2_rn(acc[i], make_float2(b[2 * i], b[2 * i + 1]));
+}
+
+// CTA pairs, 256 x 256 output tiles, TMA ring and cta_group::2 MMAs as in the int8
+// GEMM. The tensor cores sum one K block of 128 at a time (four MMAs) into one of
+// two 256-column buffers of tensor memory; the promotion warps read each block's
+// partial sums, multiply them by the block's scales and add them to fp32
+// accumulators in registers (128 columns of one row per thread), while the tensor
+// cores fill the other buffer. Per SM and K block the MMAs take 512 cycles, reading
+// 128 KB of partial sums 256, and the 128 x 256 multiply-adds 256 of the fp32
+// pipe: the tensor cores stay the bound.
+template <int EPI>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
+    gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                    const Fp8Params p) {
+  constexpr bool kSwi = EPI != kF8BF16;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* sA = smem;
+  uint8_t* sB = smem + kF8Stages * kAStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kF8Stages * kBStage);
+  uint64_t* empty = full + kF8Stages;
+  uint64_t* tfull = empty + kF8Stages;
+  uint64_t* tempty = tfull + 2;
+  uint64_t* drain = tempty + 2;
+  uint64_t* rmax_bar = drain + 1;  // [quarter]: both halves' row maxima are in shared memory
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rmax_bar + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  float* row_max = reinterpret_cast<float*>(smem + kF8Stages * kF8StageBytes + 256);  // [tile parity][half][row]
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const int pair = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  const int KB = p.KB;
+  const uint64_t limit = p.wait_limit_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kF8Stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 16);  // leader's: 8 promotion warps of each CTA
+    }
+    mbar_init(drain, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&rmax_bar[i], 2);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_slot, kTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+
+  auto tile_at = [&](int tile, int& mb, int& nb) {
+    const int per_group = p.group_m * p.num_n;
+    const int gid = tile / per_group;
+    const int first_m = gid * p.group_m;
+    const int gm = min(p.num_m - first_m, p.group_m);
+    const int r = tile - gid * per_group;
+    mb = first_m + r % gm;
+    nb = r / gm;
+  };
+
+  if (warp < 4) {
+    regs_dec<kF8RegsCtl>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ producer (both CTAs)
+      const uint64_t pol = policy_evict_last();
+      int stage = 0;
+      uint32_t phase = 0;
+      long issued = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < p.num_tiles; tile += npairs) {
+        int mb, nb;
+        tile_at(tile, mb, nb);
+        const int a_row = mb * (2 * kBM) + static_cast<int>(rank) * kBM;
+        const int b_row = kSwi ? (rank == 0 ? nb * 128 : p.b_row_up + nb * 128)
+                               : nb * kBN + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1u, limit, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_leader = cluster_map(&full[stage], 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes);
+          tma_load_2d_pair(sA + stage * kAStage, &tmA, full_leader, kb * kBK, a_row, pol);
+          tma_load_2d_pair(sB + stage * kBStage, &tmB, full_leader, kb * kBK, b_row, pol);
+          ++issued;
+          if (++stage == kF8Stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!ok && rank == 0) {
+        for (int s = 0; s < kF8Stages; ++s) {
+          if (issued <= s) continue;
+          const long last = ((issued - 1 - s) / kF8Stages) * kF8Stages + s;
+          mbar_wait_bounded(&full[s], static_cast<uint32_t>((last / kF8Stages) & 1), limit, nullptr);
+        }
+      }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ------------------------------------------------------------ MMA issuer (leader only)
+      constexpr uint32_t idesc = idesc_fp8(2 * kBM, kBN);
+      int stage = 0;
+      uint32_t phase = 0;
+      int buf = 0;
+      uint32_t buf_phase = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < p.num_tiles; tile += npairs) {
+        for (int kb = 0; kb < KB; ++kb) {
+          if (!mbar_wait_bounded_cluster(&tempty[buf], buf_phase ^ 1u, limit, abort_flag) ||
+              !mbar_wait_bounded(&full[stage], phase, limit, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t d = tmem + static_cast<uint32_t>(buf * kBN);
+          const uint64_t ad = smem_desc_sw128(smem_u32(sA + stage * kAStage));
+          const uint64_t bd = smem_desc_sw128(smem_u32(sB + stage * kBStage));
+#pragma unroll
+          for (int k = 0; k < kBK / 32; ++k) mma_fp8_pair(d, ad + 2u * k, bd + 2u * k, idesc, k != 0 ? 1u : 0u);
+          mma_commit_pair(cluster_map(&empty[stage], 0));
+          mma_commit_pair(cluster_map(&empty[stage], 1));
+          mma_commit_pair(cluster_map(&tfull[buf], 0));
+          mma_commit_pair(cluster_map(&tfull[buf], 1));
+          if (++stage == kF8Stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
+        }
+      }
+      mma_commit_pair(cluster_map(drain, 0));
+      mbar_wait_bounded(drain, 0, limit, nullptr);
+    }
+  } else {
+    regs_inc<kF8RegsPromote>();
+    // -------------------------------------------------------------- promotion and epilogue (both CTAs)
+    // Warps 4..11: warp w owns TMEM lanes 32*(w%4) .. +31 and half of the columns:
+    // columns [128 half, +128), or with SwiGLU gate [64 half, +64) (chunks 0, 1)
+    // and up [128 + 64 half, +64) (chunks 2, 3).
+    const int quarter = warp & 3;
+    const int half = (warp - 4) >> 2;
+    const int row_in_cta = quarter * 32 + lane;
+    const uint32_t tempty0 = cluster_map(&tempty[0], 0);
+    const uint32_t tempty1 = cluster_map(&tempty[1], 0);
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t col[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) col[c] = kSwi ? (c < 2 ? 64 * half + 32 * c : 128 + 64 * half + 32 * (c - 2)) : 128 * half + 32 * c;
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    int iter = 0;
+    bool ok = true;
+    for (int tile = pair; ok && tile < p.num_tiles; tile += npairs, ++iter) {
+      int mb, nb;
+      tile_at(tile, mb, nb);
+      const int row = mb * (2 * kBM) + static_cast<int>(rank) * kBM + row_in_cta;
+      const bool row_ok = row < p.M;
+      const float* sx = p.sx + (row_ok ? row : 0);
+      const float* sw0 = p.sw + int64_t(kSwi ? nb : min(2 * nb + half, p.last_nb)) * KB;
+      const float* sw1 = kSwi ? p.sw + int64_t(p.b_row_up / 128 + nb) * KB : sw0;
+      float2 acc[4][16];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c][i] = make_float2(0.0f, 0.0f);
+      float sxn = __ldg(sx), w0n = __ldg(sw0), w1n = kSwi ? __ldg(sw1) : 0.0f;
+      for (int kb = 0; kb < KB; ++kb) {
+        const float f0 = __fmul_rn(sxn, w0n);
+        const float f1 = kSwi ? __fmul_rn(sxn, w1n) : f0;
+        if (kb + 1 < KB) {  // the next block's scales load while this block is promoted
+          sxn = __ldg(sx + int64_t(kb + 1) * p.M);
+          w0n = __ldg(sw0 + kb + 1);
+          if constexpr (kSwi) w1n = __ldg(sw1 + kb + 1);
+        }
+        if (!mbar_wait_bounded_cluster(&tfull[buf], buf_phase, limit, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ta = tlane + static_cast<uint32_t>(buf * kBN);
+        uint32_t ra[32], rb[32];
+        tmem_ld32(ta + col[0], ra);
+        tmem_ld_wait32(ra);
+        tmem_ld32(ta + col[1], rb);
+        f8_promote(acc[0], ra, f0);
+        tmem_ld_wait32(rb);
+        tmem_ld32(ta + col[2], ra);
+        f8_promote(acc[1], rb, f0);
+        tmem_ld_wait32(ra);
+        tmem_ld32(ta + col[3], rb);
+        f8_promote(acc[2], ra, f1);
+        tmem_ld_wait32(rb);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(buf == 0 ? tempty0 : tempty1);
+        f8_promote(acc[3], rb, f1);
+        buf ^= 1;
+        if (buf == 0) buf_phase ^= 1u;
+      }
+      if (!ok) break;
+      if constexpr (!kSwi) {
+        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(row) * p.N;
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int n = nb * kBN + static_cast<int>(col[c]) + 8 * g;
+            if (n < p.N) {
+              float2* a = &acc[c][4 * g];
+              if (p.bias != nullptr) f8_bias8(a, p.bias + n);
+              if (row_ok)
+                *reinterpret_cast<uint4*>(out + n) = make_uint4(pack_bf16x2(a[0].x, a[0].y), pack_bf16x2(a[1].x, a[1].y),
+                                                                pack_bf16x2(a[2].x, a[2].y), pack_bf16x2(a[3].x, a[3].y));
+            }
+          }
+      } else {
+        const int n0 = nb * 128 + 64 * half;  // first h column of this thread
+        float amax = 0.0f;
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float2 *ga = &acc[c][4 * g], *ua = &acc[2 + c][4 * g];
+            if (p.bias != nullptr) {
+              f8_bias8(ga, p.bias + n0 + 32 * c + 8 * g);
+              f8_bias8(ua, p.bias + p.b_row_up + n0 + 32 * c + 8 * g);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              ga[i].x = __fmul_rn(silu_approx(ga[i].x), ua[i].x);
+              ga[i].y = __fmul_rn(silu_approx(ga[i].y), ua[i].y);
+              if constexpr (EPI == kF8SwiGLUQuant) amax = max_nan(amax, max_nan(fabsf(ga[i].x), fabsf(ga[i].y)));
+            }
+            if constexpr (EPI == kF8SwiGLU) {
+              __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(row) * p.N + n0 + 32 * c + 8 * g;
+              if (row_ok)
+                *reinterpret_cast<uint4*>(out) =
+                    make_uint4(pack_bf16x2(ga[0].x, ga[0].y), pack_bf16x2(ga[1].x, ga[1].y),
+                               pack_bf16x2(ga[2].x, ga[2].y), pack_bf16x2(ga[3].x, ga[3].y));
+            }
+          }
+        if constexpr (EPI == kF8SwiGLUQuant) {
+          // the row's 128 h columns are one scale block; its two halves sit in two warps
+          float* mine = row_max + (iter & 1) * 256 + half * 128 + row_in_cta;
+          *mine = amax;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rmax_bar[quarter]);
+          if (!mbar_wait_bounded(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
+          amax = max_nan(amax, row_max[(iter & 1) * 256 + (half ^ 1) * 128 + row_in_cta]);
+          float inv;
+          const float s = fp8_scale(amax, inv);
+          if (row_ok) {
+            uint8_t* out = static_cast<uint8_t*>(p.out) + int64_t(row) * p.N + n0;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 a = acc[g >> 1][8 * (g & 1) + 2 * i], b = acc[g >> 1][8 * (g & 1) + 2 * i + 1];
+                w[i] = f32x4_to_e4m3x4(__fmul_rn(a.x, inv), __fmul_rn(a.y, inv), __fmul_rn(b.x, inv),
+                                       __fmul_rn(b.y, inv));
+              }
+              *reinterpret_cast<uint4*>(out + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (half == 0) p.sh[int64_t(nb) * p.M + row] = s;
+          }
+        }
+      }
+    }
+  }
+
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+}  // namespace h3q

@@ -1,6 +1,6 @@
 // libh3q.so: the C ABI declared in include/h3q.h. Host-side argument checks,
-// TMA descriptor setup and launches of the kernels in rotquant.cuh and
-// gemm_sm100.cuh. Everything is stream-ordered; nothing here allocates device
+// TMA descriptor setup and launches of the kernels in the .cuh files
+// beside it. Everything is stream-ordered; nothing here allocates device
 // memory.
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -18,6 +18,8 @@
 #include "lora.cuh"
 #include "nvfp4.cuh"
 #include "attention.cuh"
+#include "fp8.cuh"
+#include "qk_norm_rope.cuh"
 #include "rotquant.cuh"
 
 namespace {
@@ -184,6 +186,55 @@ h3q_status launch_gemm_fp4(const uint8_t* a, const uint8_t* a_sf, const float* a
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
   h3q::gemm_fp4_kernel<EPI><<<2 * pairs, h3q::kF4Threads, h3q::kF4Smem, stream>>>(ta, tb, tsa, tsb, p);
   return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+}
+
+template <int EPI>
+h3q_status launch_gemm_fp8(const uint8_t* a, const float* sx, int64_t M, int64_t K, const uint8_t* b, const float* sw,
+                           int64_t b_rows, int64_t N_out, const void* bias, void* out, float* sh,
+                           cudaStream_t stream) {
+  CUtensorMap ta, tb;
+  if (!make_tmap_i8(&ta, a, M, K) || !make_tmap_i8(&tb, b, b_rows, K)) return H3Q_ERR_CUDA;
+  const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_kernel<EPI>);
+  if (ensure_smem_attr(kernel, static_cast<int>(h3q::kF8Smem)) != cudaSuccess) return H3Q_ERR_CUDA;
+  // the kernel's register split assumes this many registers per thread at launch
+  static std::once_flag regs_once;
+  static bool regs_ok = false;
+  std::call_once(regs_once, [kernel] {
+    cudaFuncAttributes fa{};
+    regs_ok = cudaFuncGetAttributes(&fa, kernel) == cudaSuccess && fa.numRegs >= static_cast<int>(h3q::kF8RegsLaunch);
+  });
+  if (!regs_ok) return H3Q_ERR_UNSUPPORTED;
+  h3q::Fp8Params p{};
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N_out);
+  p.K = static_cast<int>(K);
+  p.KB = static_cast<int>((K + 127) / 128);
+  p.num_m = static_cast<int>((M + 2 * h3q::kBM - 1) / (2 * h3q::kBM));
+  p.num_n = (EPI == h3q::kF8BF16) ? static_cast<int>((N_out + h3q::kBN - 1) / h3q::kBN)
+                                  : static_cast<int>(N_out / 128);
+  p.num_tiles = p.num_m * p.num_n;
+  p.group_m = kGemmGroupRows < p.num_m ? kGemmGroupRows : p.num_m;
+  p.b_row_up = (EPI == h3q::kF8BF16) ? 0 : static_cast<int>(N_out);
+  p.last_nb = static_cast<int>((b_rows + 127) / 128) - 1;
+  p.sx = sx;
+  p.sw = sw;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.out = out;
+  p.sh = sh;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  const int sms = sm_count();
+  if (sms <= 0) return H3Q_ERR_CUDA;
+  const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
+  h3q::gemm_fp8_kernel<EPI><<<2 * pairs, h3q::kF8Threads, h3q::kF8Smem, stream>>>(ta, tb, p);
+  return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+}
+
+template <int G>
+void launch_qk(const h3q::QkParams& p, bool interleaved, unsigned grid, cudaStream_t stream) {
+  if (interleaved)
+    h3q::qk_norm_rope_kernel<G, true><<<grid, 256, 0, stream>>>(p);
+  else
+    h3q::qk_norm_rope_kernel<G, false><<<grid, 256, 0, stream>>>(p);
 }
 
 // [rows, cols] bf16 row-major, boxes of 64 columns (128 bytes) x 128 rows,
@@ -462,6 +513,133 @@ h3q_status h3q_gemm_nvfp4_f32(const uint8_t* xc, const uint8_t* xsf, int64_t M, 
   if (st != H3Q_OK || M == 0) return st;
   if (!acc || !aligned16(acc)) return H3Q_ERR_INVALID_ARG;
   return launch_gemm_fp4<h3q::kEpiS32>(xc, xsf, nullptr, M, K, wc, wsf, nullptr, N, N, nullptr, acc, stream);
+}
+
+// K of the fp8 calls: rows of codes start on 16 bytes.
+static bool valid_fp8_k(int64_t K) { return K >= 16 && K % 16 == 0; }
+
+static h3q_status fp8_quantize_any(bool weight, const void* x, int x_dtype, int64_t rows, int64_t K, uint8_t* codes,
+                                   float* scales, cudaStream_t stream) {
+  if (rows < 0 || !valid_fp8_k(K) || (x_dtype != H3Q_DTYPE_BF16 && x_dtype != H3Q_DTYPE_F32))
+    return H3Q_ERR_INVALID_ARG;
+  if (rows > INT32_MAX - 256 || K > INT32_MAX - 256) return H3Q_ERR_UNSUPPORTED;
+  if (rows == 0) return H3Q_OK;
+  if (!x || !codes || !scales || !aligned16(x) || !aligned16(codes) || !aligned16(scales)) return H3Q_ERR_INVALID_ARG;
+  const int KB = static_cast<int>((K + 127) / 128);
+  const __nv_bfloat16* xb = static_cast<const __nv_bfloat16*>(x);
+  const float* xf = static_cast<const float*>(x);
+  const int k = static_cast<int>(K);
+  if (weight) {
+    const int64_t blocks = (rows + 127) / 128 * KB;
+    if (blocks > INT32_MAX) return H3Q_ERR_UNSUPPORTED;
+    const unsigned g = static_cast<unsigned>(blocks);
+    if (x_dtype == H3Q_DTYPE_BF16)
+      h3q::fp8_weight_kernel<__nv_bfloat16><<<g, 256, 0, stream>>>(xb, rows, k, KB, codes, scales);
+    else
+      h3q::fp8_weight_kernel<float><<<g, 256, 0, stream>>>(xf, rows, k, KB, codes, scales);
+  } else {
+    const int sms = sm_count();
+    if (sms <= 0) return H3Q_ERR_CUDA;
+    const unsigned g = static_cast<unsigned>(std::min<int64_t>((rows * KB + 15) / 16, int64_t(sms) * 8));
+    if (x_dtype == H3Q_DTYPE_BF16)
+      h3q::fp8_quantize_kernel<__nv_bfloat16><<<g, 256, 0, stream>>>(xb, rows, k, KB, codes, scales);
+    else
+      h3q::fp8_quantize_kernel<float><<<g, 256, 0, stream>>>(xf, rows, k, KB, codes, scales);
+  }
+  return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+}
+
+h3q_status h3q_fp8_quantize(const void* x, int x_dtype, int64_t M, int64_t K, uint8_t* xq, float* sx,
+                            cudaStream_t stream) {
+  return fp8_quantize_any(false, x, x_dtype, M, K, xq, sx, stream);
+}
+
+h3q_status h3q_fp8_prepare_weight(const void* w, int w_dtype, int64_t N, int64_t K, uint8_t* wq, float* sw,
+                                  cudaStream_t stream) {
+  return fp8_quantize_any(true, w, w_dtype, N, K, wq, sw, stream);
+}
+
+static h3q_status check_fp8_args(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq,
+                                 const float* sw, int64_t N, const void* bias) {
+  if (M < 0 || !valid_fp8_k(K) || N <= 0 || N % 8 != 0) return H3Q_ERR_INVALID_ARG;
+  if (M > INT32_MAX - 256 || N > INT32_MAX - 512 || K > INT32_MAX - 256) return H3Q_ERR_UNSUPPORTED;
+  if (((M + 255) / 256) * ((N + 127) / 128) > INT32_MAX / 2) return H3Q_ERR_UNSUPPORTED;
+  if (M == 0) return H3Q_OK;
+  if (!xq || !sx || !wq || !sw || !aligned16(xq) || !aligned16(sx) || !aligned16(wq) || !aligned16(sw) ||
+      (bias && !aligned16(bias)))
+    return H3Q_ERR_INVALID_ARG;
+  return H3Q_OK;
+}
+
+h3q_status h3q_linear_fp8(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq, const float* sw,
+                          int64_t N, const void* bias_bf16, int epilogue, void* y_bf16, cudaStream_t stream) {
+  if (epilogue != H3Q_EPI_NONE && epilogue != H3Q_EPI_SWIGLU) return H3Q_ERR_INVALID_ARG;
+  if (epilogue == H3Q_EPI_SWIGLU && N % 256 != 0) return H3Q_ERR_INVALID_ARG;
+  const h3q_status st = check_fp8_args(xq, sx, M, K, wq, sw, N, bias_bf16);
+  if (st != H3Q_OK || M == 0) return st;
+  if (!y_bf16 || !aligned16(y_bf16)) return H3Q_ERR_INVALID_ARG;
+  if (epilogue == H3Q_EPI_SWIGLU)
+    return launch_gemm_fp8<h3q::kF8SwiGLU>(xq, sx, M, K, wq, sw, N, N / 2, bias_bf16, y_bf16, nullptr, stream);
+  return launch_gemm_fp8<h3q::kF8BF16>(xq, sx, M, K, wq, sw, N, N, bias_bf16, y_bf16, nullptr, stream);
+}
+
+h3q_status h3q_linear_fp8_swiglu_quant(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq,
+                                       const float* sw, int64_t N, const void* bias_bf16, uint8_t* hq, float* sh,
+                                       cudaStream_t stream) {
+  if (N % 256 != 0) return H3Q_ERR_INVALID_ARG;
+  const h3q_status st = check_fp8_args(xq, sx, M, K, wq, sw, N, bias_bf16);
+  if (st != H3Q_OK || M == 0) return st;
+  if (!hq || !sh || !aligned16(hq) || !aligned16(sh)) return H3Q_ERR_INVALID_ARG;
+  return launch_gemm_fp8<h3q::kF8SwiGLUQuant>(xq, sx, M, K, wq, sw, N, N / 2, bias_bf16, hq, sh, stream);
+}
+
+h3q_status h3q_qk_norm_rope(const void* q, const void* k, int64_t S, int64_t Hq, int64_t Hk, int64_t D, int64_t ldq,
+                            int64_t ldk, const void* q_weight, const void* k_weight, float eps, const float* cos,
+                            const float* sin, int64_t P, int64_t rot, int interleaved, const int32_t* positions,
+                            void* q_out, void* k_out, int64_t ldq_out, int64_t ldk_out, cudaStream_t stream) {
+  if (S < 0 || Hq < 1 || Hk < 0 || D < 16 || D % 16 != 0 || rot < 0 || rot % 16 != 0 || rot > D) return H3Q_ERR_INVALID_ARG;
+  if (D > H3Q_QK_MAX_D || Hq > H3Q_QK_MAX_HEADS || Hk > H3Q_QK_MAX_HEADS || S > INT32_MAX - 256 || P > INT32_MAX)
+    return H3Q_ERR_UNSUPPORTED;
+  if (ldq < Hq * D || ldq_out < Hq * D || ldq % 8 != 0 || ldq_out % 8 != 0) return H3Q_ERR_INVALID_ARG;
+  if (Hk > 0 && (ldk < Hk * D || ldk_out < Hk * D || ldk % 8 != 0 || ldk_out % 8 != 0)) return H3Q_ERR_INVALID_ARG;
+  if (!(eps >= 0.0f) || std::isinf(eps)) return H3Q_ERR_INVALID_ARG;
+  if (S == 0) return H3Q_OK;
+  if (!q || !q_out || !aligned16(q) || !aligned16(q_out)) return H3Q_ERR_INVALID_ARG;
+  if (Hk > 0 && (!k || !k_out || !aligned16(k) || !aligned16(k_out))) return H3Q_ERR_INVALID_ARG;
+  if ((q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight))) return H3Q_ERR_INVALID_ARG;
+  if (rot > 0 && (!cos || !sin || !aligned16(cos) || !aligned16(sin) || P < 1 || (!positions && P < S)))
+    return H3Q_ERR_INVALID_ARG;
+  if (positions && (reinterpret_cast<uintptr_t>(positions) & 3u) != 0) return H3Q_ERR_INVALID_ARG;
+  h3q::QkParams p{};
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.qo = static_cast<__nv_bfloat16*>(q_out);
+  p.ko = static_cast<__nv_bfloat16*>(k_out);
+  p.ldq = ldq;
+  p.ldk = ldk;
+  p.ldqo = ldq_out;
+  p.ldko = ldk_out;
+  p.wq = static_cast<const __nv_bfloat16*>(q_weight);
+  p.wk = static_cast<const __nv_bfloat16*>(k_weight);
+  p.cos = cos;
+  p.sin = sin;
+  p.pos = rot > 0 ? positions : nullptr;
+  p.S = S;
+  p.Hq = static_cast<int>(Hq);
+  p.Hk = static_cast<int>(Hk);
+  p.D = static_cast<int>(D);
+  p.rot = static_cast<int>(rot);
+  p.P = static_cast<int>(P);
+  p.eps = eps;
+  const int sms = sm_count();
+  if (sms <= 0) return H3Q_ERR_CUDA;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((S + 7) / 8, int64_t(sms) * 8));
+  const bool il = interleaved != 0;
+  if (D <= 32) launch_qk<4>(p, il, grid, stream);
+  else if (D <= 64) launch_qk<8>(p, il, grid, stream);
+  else if (D <= 128) launch_qk<16>(p, il, grid, stream);
+  else launch_qk<32>(p, il, grid, stream);
+  return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
 
 struct AttLayout {
