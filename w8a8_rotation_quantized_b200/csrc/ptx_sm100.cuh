@@ -123,6 +123,15 @@ __device__ __forceinline__ bool mbar_wait_bounded_lazy(uint64_t* bar, uint32_t p
   return true;
 }
 
+// True in one lane of a converged warp. A role that its whole warp runs, with only
+// the instructions themselves under this predicate, keeps its addresses and
+// descriptors in uniform registers, where the tcgen05 and TMA instructions take them.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- register split
 template <uint32_t N>
 __device__ __forceinline__ void regs_dec() {
@@ -131,6 +140,13 @@ __device__ __forceinline__ void regs_dec() {
 template <uint32_t N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// mbar_wait_bounded_lazy for a converged warp that waits as one: the result is the
+// same in every lane, and the warp is converged again afterwards.
+__device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
+                                                       volatile int* abort) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait_bounded_lazy(bar, parity, limit_ns, abort));
 }
 
 // ---------------------------------------------------------------- clusters
@@ -187,6 +203,14 @@ __device__ __forceinline__ bool mbar_wait_bounded_cluster(uint64_t* bar, uint32_
       }
     }
   }
+}
+
+// Arrive on an mbarrier of any CTA of the cluster, ordering only tensor-memory
+// accesses (which tcgen05.fence and the MMA's own completion order), no other
+// memory: a release at cluster scope waits for all of the thread's earlier memory
+// operations, which costs more than a K block's products.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // ---------------------------------------------------------------- TMA
@@ -327,6 +351,15 @@ __device__ __forceinline__ void mma_commit_pair(uint32_t bar_cluster_addr) {
   asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
                    bar_cluster_addr)
                : "memory");
+}
+
+// mma_commit_pair on the barriers at `bar`'s offset in both CTAs of the pair.
+__device__ __forceinline__ void mma_commit_pair_both(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"(static_cast<uint16_t>(3))
+      : "memory");
 }
 
 // Each lane of the warp reads 32 consecutive 32-bit columns of its own TMEM lane.
