@@ -194,12 +194,36 @@ __device__ __forceinline__ float silu_approx(float g) {
   return __fmul_rn(g, r);
 }
 
+__device__ __forceinline__ uint4 f8_pack8(const float* a) {
+  return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
+                    pack_bf16x2(a[6], a[7]));
+}
+
+// Adds eight bias values to acc[0 .. 7].
+__device__ __forceinline__ void f8_bias8(float* acc, const __nv_bfloat16* bias) {
+  float b[8];
+  fp8_load8(bias, b);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], b[i]);
+}
+
+__device__ __forceinline__ void f8_bias32(float* acc, const __nv_bfloat16* bias) {
+#pragma unroll
+  for (int g = 0; g < 4; ++g) f8_bias8(acc + 8 * g, bias + 8 * g);
+}
+
 enum Fp8Epi : int { kF8BF16 = 0, kF8SwiGLU = 1, kF8SwiGLUQuant = 2 };
 
-constexpr int kF8Stages = 6;
-constexpr int kF8Threads = 384;  // producer, MMA, two idle warps, 8 promotion warps
+constexpr int kF8Stages = 5;
+constexpr int kF8Threads = 384;  // 8 promotion warps, then two producers and two MMA issuers
+constexpr int kF8Producer = 8, kF8Issuer = 10;
 constexpr int kF8StageBytes = kAStage + kBStage;
-constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + 1024 /*align*/ + 256 /*barriers*/ + 2 * 2 * 128 * 4;
+constexpr int kF8ScaleKB = 8;                            // K blocks whose scales are fetched together
+constexpr int kF8ScaleSlot = (kF8ScaleKB * 32 + 32) * 4;  // a warp's 32 rows of them, then two weight blocks' (and padding)
+constexpr int kF8OutTile = 32 * 128;                     // a warp's 32 output rows of 128 bytes
+constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + 8 * kF8OutTile + 8 * 2 * kF8ScaleSlot +
+                           2 * 2 * 128 * 4 /*row maxima*/ + 256 /*barriers*/ + 1024 /*align*/;
+static_assert(kF8Smem <= 232448, "shared memory of one CTA");
 // Register split: the launch's 168 per thread, moved from the first warpgroup to
 // the two that hold accumulators.
 constexpr uint32_t kF8RegsCtl = 40, kF8RegsPromote = 232, kF8RegsLaunch = 168;
@@ -226,19 +250,6 @@ __device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&r)
   for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(r[i]), f, acc[i]);
 }
 
-__device__ __forceinline__ uint4 f8_pack8(const float* a) {
-  return make_uint4(pack_bf16x2(a[0], a[1]), pack_bf16x2(a[2], a[3]), pack_bf16x2(a[4], a[5]),
-                    pack_bf16x2(a[6], a[7]));
-}
-
-// Adds eight bias values to acc[0 .. 7].
-__device__ __forceinline__ void f8_bias8(float* acc, const __nv_bfloat16* bias) {
-  float b[8];
-  fp8_load8(bias, b);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) acc[i] = __fadd_rn(acc[i], b[i]);
-}
-
 // CTA pairs, 256 x 256 output tiles, TMA ring and cta_group::2 MMAs as in the int8
 // GEMM. The tensor cores sum one K block of 128 at a time (four MMAs) into one of
 // two 256-column buffers of tensor memory; the promotion warps read each block's
@@ -256,7 +267,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kF8Stages * kAStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(sB + kF8Stages * kBStage);
+  uint8_t* out_tiles = sB + kF8Stages * kBStage;    // [warp]
+  uint8_t* scale_slots = out_tiles + 8 * kF8OutTile;  // [warp][2]
+  float* row_max = reinterpret_cast<float*>(scale_slots + 8 * 2 * kF8ScaleSlot);  // [tile parity][half][row]
+  uint64_t* full = reinterpret_cast<uint64_t*>(row_max + 2 * 2 * 128);
   uint64_t* empty = full + kF8Stages;
   uint64_t* tfull = empty + kF8Stages;
   uint64_t* tempty = tfull + 2;
@@ -264,7 +278,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   uint64_t* rmax_bar = drain + 1;  // [quarter]: both halves' row maxima are in shared memory
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rmax_bar + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  float* row_max = reinterpret_cast<float*>(smem + kF8Stages * kF8StageBytes + 256);  // [tile parity][half][row]
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
   const uint32_t rank = cluster_ctarank();
@@ -281,16 +294,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
       mbar_init(&tfull[b], 1);
       mbar_init(&tempty[b], 16);  // leader's: 8 promotion warps of each CTA
     }
-    mbar_init(drain, 1);
+    mbar_init(drain, 2);  // the two issuers
     for (int i = 0; i < 4; ++i) mbar_init(&rmax_bar[i], 2);
     *abort_flag = 0;
     fence_mbarrier_init();
   }
-  if (warp == 0 && lane == 0) {
+  if (warp == kF8Producer && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
   }
-  if (warp == 1) {
+  if (warp == kF8Issuer) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
     tmem_relinquish_pair();
   }
@@ -309,222 +322,271 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     nb = r / gm;
   };
 
-  if (warp < 4) {
+  if (warp >= 8) {
     regs_dec<kF8RegsCtl>();
-    if (warp == 0) {
-      // ------------------------------------------------------------ producer (both CTAs)
+    const int my_tiles = pair < p.num_tiles ? (p.num_tiles - pair + npairs - 1) / npairs : 0;
+    const int total = my_tiles * KB;  // K blocks of all of this pair's tiles, in order
+    if (warp < kF8Issuer) {
+      // ------------------------------------------------------------ producers (both CTAs): K blocks of one parity each
       const bool one = elect_one();
       const uint64_t pol = policy_evict_last();
-      int stage = 0;
+      const int par = warp - kF8Producer;
+      int stage = par;
       uint32_t phase = 0;
-      long issued = 0;
-      bool ok = true;
-      for (int tile = pair; ok && tile < p.num_tiles; tile += npairs) {
-        int mb, nb;
-        tile_at(tile, mb, nb);
-        const int a_row = mb * (2 * kBM) + static_cast<int>(rank) * kBM;
-        const int b_row = kSwi ? (rank == 0 ? nb * 128 : p.b_row_up + nb * 128)
-                               : nb * kBN + static_cast<int>(rank) * 128;
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1u, limit, abort_flag)) {
-            ok = false;
-            break;
-          }
-          const uint32_t full_leader = cluster_map(&full[stage], 0);
-          if (one) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes);
-            tma_load_2d_pair(sA + stage * kAStage, &tmA, full_leader, kb * kBK, a_row, pol);
-            tma_load_2d_pair(sB + stage * kBStage, &tmB, full_leader, kb * kBK, b_row, pol);
-          }
-          ++issued;
-          if (++stage == kF8Stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
+      int kb = par, tile = pair, a_row = 0, b_row = 0;
+      bool moved = true;
+      int n = par;
+      for (; n < total; n += 2, kb += 2) {
+        while (kb >= KB) {
+          kb -= KB;
+          tile += npairs;
+          moved = true;
+        }
+        if (moved) {
+          int mb, nb;
+          tile_at(tile, mb, nb);
+          a_row = mb * (2 * kBM) + static_cast<int>(rank) * kBM;
+          b_row = kSwi ? (rank == 0 ? nb * 128 : p.b_row_up + nb * 128) : nb * kBN + static_cast<int>(rank) * 128;
+          moved = false;
+        }
+        if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1u, limit, abort_flag)) break;
+        const uint32_t full_leader = cluster_map(&full[stage], 0);
+        if (one) {
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes);
+          tma_load_2d_pair(sA + stage * kAStage, &tmA, full_leader, kb * kBK, a_row, pol);
+          tma_load_2d_pair(sB + stage * kBStage, &tmB, full_leader, kb * kBK, b_row, pol);
+        }
+        stage += 2;
+        if (stage >= kF8Stages) {
+          stage -= kF8Stages;
+          phase ^= 1u;
         }
       }
-      if (!ok && rank == 0) {
-        for (int s = 0; s < kF8Stages; ++s) {
-          if (issued <= s) continue;
-          const long last = ((issued - 1 - s) / kF8Stages) * kF8Stages + s;
-          mbar_wait_bounded(&full[s], static_cast<uint32_t>((last / kF8Stages) & 1), limit, nullptr);
-        }
+      if (n < total && rank == 0) {
+        // drain this producer's copies that may still be in flight (bounded, ignores abort)
+        for (int m = n - 2; m >= 0 && m > n - 2 - kF8Stages; m -= 2)
+          mbar_wait_bounded(&full[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr);
       }
-    } else if (warp == 1 && rank == 0) {
-      // ------------------------------------------------------------ MMA issuer (leader only)
+    } else if (rank == 0) {
+      // ------------------------------------------------------------ MMA issuers (leader only): one accumulator buffer each
       constexpr uint32_t idesc = idesc_fp8(2 * kBM, kBN);
       const bool one = elect_one();
-      int stage = 0;
-      uint32_t phase = 0;
-      int buf = 0;
-      uint32_t buf_phase = 0;
-      bool ok = true;
-      for (int tile = pair; ok && tile < p.num_tiles; tile += npairs) {
-        for (int kb = 0; kb < KB; ++kb) {
-          if (!mbar_wait_bounded_warp(&tempty[buf], buf_phase ^ 1u, limit, abort_flag) ||
-              !mbar_wait_bounded_warp(&full[stage], phase, limit, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t d = tmem + static_cast<uint32_t>(buf * kBN);
-          const uint64_t ad = smem_desc_sw128(smem_u32(sA + stage * kAStage));
-          const uint64_t bd = smem_desc_sw128(smem_u32(sB + stage * kBStage));
-          if (one) {
+      const int buf = warp - kF8Issuer;
+      const uint32_t d = tmem + static_cast<uint32_t>(buf * kBN);
+      const uint64_t ad0 = smem_desc_sw128(smem_u32(sA)), bd0 = smem_desc_sw128(smem_u32(sB));
+      int stage = buf;
+      uint32_t phase = 0, buf_phase = 0;
+      for (int n = buf; n < total; n += 2) {
+        if (!mbar_wait_bounded_warp(&full[stage], phase, limit, abort_flag) ||
+            !mbar_wait_bounded_warp(&tempty[buf], buf_phase ^ 1u, limit, abort_flag))
+          break;
+        tc_fence_after();
+        const uint64_t ad = ad0 + static_cast<uint32_t>(stage * (kAStage >> 4));
+        const uint64_t bd = bd0 + static_cast<uint32_t>(stage * (kBStage >> 4));
+        if (one) {
 #pragma unroll
-            for (int k = 0; k < kBK / 32; ++k) mma_fp8_pair(d, ad + 2u * k, bd + 2u * k, idesc, k != 0 ? 1u : 0u);
-            mma_commit_pair_both(&empty[stage]);
-            mma_commit_pair_both(&tfull[buf]);
-          }
-          if (++stage == kF8Stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          buf ^= 1;
-          if (buf == 0) buf_phase ^= 1u;
+          for (int k = 0; k < kBK / 32; ++k) mma_fp8_pair(d, ad + 2u * k, bd + 2u * k, idesc, k != 0 ? 1u : 0u);
+          mma_commit_pair_both(&tfull[buf]);
+          mma_commit_pair_both(&empty[stage]);
+        }
+        buf_phase ^= 1u;
+        stage += 2;
+        if (stage >= kF8Stages) {
+          stage -= kF8Stages;
+          phase ^= 1u;
         }
       }
       if (one) mma_commit_pair(cluster_map(drain, 0));
-      mbar_wait_bounded(drain, 0, limit, nullptr);
+      mbar_wait_bounded(drain, 0, limit, nullptr);  // both issuers' MMAs are done
     }
   } else {
     regs_inc<kF8RegsPromote>();
     // -------------------------------------------------------------- promotion and epilogue (both CTAs)
-    // Warps 4..11: warp w owns TMEM lanes 32*(w%4) .. +31 and, of each buffer,
+    // Warps 0..7: warp w owns TMEM lanes 32*(w%4) .. +31 and, of each buffer,
     // columns [64 half, +64) (chunks 0, 1: gate with SwiGLU) and
     // [128 + 64 half, +64) (chunks 2, 3: up).
     const int quarter = warp & 3;
-    const int half = (warp - 4) >> 2;
+    const int half = warp >> 2;
     const int row_in_cta = quarter * 32 + lane;
     const uint32_t tempty0 = cluster_map(&tempty[0], 0);
     const uint32_t tempty1 = cluster_map(&tempty[1], 0);
     const uint32_t tlane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(64 * half);
-    int col[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) col[c] = 64 * half + 32 * (c & 1) + 128 * (c >> 1);
-    int buf = 0;
-    uint32_t buf_phase = 0;
-    int iter = 0;
-    bool ok = true;
-    for (int tile = pair; ok && tile < p.num_tiles; tile += npairs, ++iter) {
+    uint8_t* out_tile = out_tiles + warp * kF8OutTile;
+    uint8_t* slots = scale_slots + warp * 2 * kF8ScaleSlot;
+    // Scales of K blocks kb0 .. kb0 + 7 of a tile into a slot, in flight until the slot's
+    // turn comes: each lane its own row's (zero past the end of M or K), lanes 0-15 the
+    // two weight blocks'.
+    auto fetch_scales = [&](int tile, int kb0, int slot) {
       int mb, nb;
       tile_at(tile, mb, nb);
       const int row = mb * (2 * kBM) + static_cast<int>(rank) * kBM + row_in_cta;
-      const bool row_ok = row < p.M;
-      const float* sx = p.sx + (row_ok ? row : 0);
-      const int nb0 = kSwi ? nb : 2 * nb, nb1 = kSwi ? p.b_row_up / 128 + nb : min(2 * nb + 1, p.last_nb);
-      const float* sw0 = p.sw + int64_t(nb0) * KB;
-      const float* sw1 = p.sw + int64_t(nb1) * KB;
+      const uint32_t dst = smem_u32(slots + slot * kF8ScaleSlot);
+      const float* sx = p.sx + int64_t(kb0) * p.M + (row < p.M ? row : 0);
+#pragma unroll
+      for (int j = 0; j < kF8ScaleKB; ++j) {
+        const bool in = kb0 + j < KB;
+        cp_async4(dst + (j * 32 + lane) * 4, in ? sx + int64_t(j) * p.M : p.sx, in && row < p.M);
+      }
+      if (lane < 2 * kF8ScaleKB) {
+        const int j = lane & (kF8ScaleKB - 1), which = lane / kF8ScaleKB;
+        const int nbw = kSwi ? (which ? p.b_row_up / 128 + nb : nb) : min(2 * nb + which, p.last_nb);
+        const bool in = kb0 + j < KB;
+        cp_async4(dst + (kF8ScaleKB * 32 + lane) * 4, in ? p.sw + int64_t(nbw) * KB + kb0 + j : p.sw, in);
+      }
+      cp_async_commit();
+    };
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    int iter = 0, slot = 0;
+    bool ok = true;
+    if (pair < p.num_tiles) fetch_scales(pair, 0, 0);
+    for (int tile = pair; ok && tile < p.num_tiles; tile += npairs, ++iter) {
+      int mb, nb;
+      tile_at(tile, mb, nb);
       float acc[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-      float sxn = __ldg(sx), w0n = __ldg(sw0), w1n = __ldg(sw1);
-      for (int kb = 0; kb < KB; ++kb) {
-        const float f0 = __fmul_rn(sxn, w0n);
-        const float f1 = __fmul_rn(sxn, w1n);
-        if (kb + 1 < KB) {  // the next block's scales load while this block is promoted
-          sxn = __ldg(sx + int64_t(kb + 1) * p.M);
-          w0n = __ldg(sw0 + kb + 1);
-          w1n = __ldg(sw1 + kb + 1);
+      for (int kb0 = 0; ok && kb0 < KB; kb0 += kF8ScaleKB) {
+        cp_async_wait_all();
+        __syncwarp();  // this slot is written, and the other one has been read by every lane
+        const float* sc = reinterpret_cast<const float*>(slots + slot * kF8ScaleSlot);
+        slot ^= 1;
+        if (kb0 + kF8ScaleKB < KB)
+          fetch_scales(tile, kb0 + kF8ScaleKB, slot);
+        else if (tile + npairs < p.num_tiles)
+          fetch_scales(tile + npairs, 0, slot);
+        const int nkb = min(kF8ScaleKB, KB - kb0);
+#pragma unroll 1
+        for (int j = 0; j < nkb; ++j) {
+          const float sxv = sc[j * 32 + lane];
+          const float f0 = __fmul_rn(sxv, sc[kF8ScaleKB * 32 + j]);
+          const float f1 = __fmul_rn(sxv, sc[kF8ScaleKB * 33 + j]);
+          if (!mbar_wait_bounded_lazy(&tfull[buf], buf_phase, limit, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t ta = tlane + static_cast<uint32_t>(buf * kBN);
+          uint32_t ra[32], rb[32];
+          tmem_ld32(ta, ra);
+          tmem_ld_wait32(ra);
+          tmem_ld32(ta + 32, rb);
+          f8_promote(acc[0], ra, f0);
+          tmem_ld_wait32(rb);
+          tmem_ld32(ta + 128, ra);
+          f8_promote(acc[1], rb, f0);
+          tmem_ld_wait32(ra);
+          tmem_ld32(ta + 160, rb);
+          f8_promote(acc[2], ra, f1);
+          tmem_ld_wait32(rb);
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(buf == 0 ? tempty0 : tempty1);
+          f8_promote(acc[3], rb, f1);
+          buf ^= 1;
+          if (buf == 0) buf_phase ^= 1u;
         }
-        if (!mbar_wait_bounded_lazy(&tfull[buf], buf_phase, limit, abort_flag)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t ta = tlane + static_cast<uint32_t>(buf * kBN);
-        uint32_t ra[32], rb[32];
-        tmem_ld32(ta, ra);
-        tmem_ld_wait32(ra);
-        tmem_ld32(ta + 32, rb);
-        f8_promote(acc[0], ra, f0);
-        tmem_ld_wait32(rb);
-        tmem_ld32(ta + 128, ra);
-        f8_promote(acc[1], rb, f0);
-        tmem_ld_wait32(ra);
-        tmem_ld32(ta + 160, rb);
-        f8_promote(acc[2], ra, f1);
-        tmem_ld_wait32(rb);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_remote(buf == 0 ? tempty0 : tempty1);
-        f8_promote(acc[3], rb, f1);
-        buf ^= 1;
-        if (buf == 0) buf_phase ^= 1u;
       }
       if (!ok) break;
-      if constexpr (!kSwi) {
-        __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(row) * p.N;
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            const int n = nb * kBN + col[c] + 8 * g;
-            if (n < p.N) {
-              float* a = &acc[c][8 * g];
-              if (p.bias != nullptr) f8_bias8(a, p.bias + n);
-              if (row_ok) *reinterpret_cast<uint4*>(out + n) = f8_pack8(a);
-            }
-          }
-      } else {
+
+      // Epilogue: the warp's 32 rows go through its shared-memory tile, 128 bytes a row
+      // with 16-byte chunks swizzled by the row, and leave as whole lines.
+      const int row0 = mb * (2 * kBM) + static_cast<int>(rank) * kBM + quarter * 32;
+      if constexpr (EPI == kF8SwiGLUQuant) {
         const int n0 = nb * 128 + 64 * half;  // first h column of this thread
         float amax = 0.0f;
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
+        for (int c = 0; c < 2; ++c) {
+          if (p.bias != nullptr) {
+            f8_bias32(acc[c], p.bias + n0 + 32 * c);
+            f8_bias32(acc[2 + c], p.bias + p.b_row_up + n0 + 32 * c);
+          }
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float *ga = &acc[c][8 * g], *ua = &acc[2 + c][8 * g];
-            if (p.bias != nullptr) {
-              f8_bias8(ga, p.bias + n0 + 32 * c + 8 * g);
-              f8_bias8(ua, p.bias + p.b_row_up + n0 + 32 * c + 8 * g);
+          for (int i = 0; i < 32; ++i) {
+            acc[c][i] = __fmul_rn(silu_approx(acc[c][i]), acc[2 + c][i]);
+            amax = max_nan(amax, fabsf(acc[c][i]));
+          }
+        }
+        // the row's 128 h columns are one scale block; its two halves sit in two warps
+        float* maxima = row_max + (iter & 1) * 256;
+        maxima[half * 128 + row_in_cta] = amax;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&rmax_bar[quarter]);
+        if (!mbar_wait_bounded_lazy(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
+        amax = max_nan(amax, maxima[(half ^ 1) * 128 + row_in_cta]);
+        float inv;
+        const float s = fp8_scale(amax, inv);
+        if (half == 0 && row0 + lane < p.M) p.sh[int64_t(nb) * p.M + row0 + lane] = s;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {  // 64 bytes a row, two rows to a 128-byte line
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* a = &acc[g >> 1][16 * (g & 1) + 4 * i];
+            w[i] = f32x4_to_e4m3x4(__fmul_rn(a[0], inv), __fmul_rn(a[1], inv), __fmul_rn(a[2], inv),
+                                   __fmul_rn(a[3], inv));
+          }
+          *reinterpret_cast<uint4*>(out_tile + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) =
+              make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 8 * i + (lane >> 2), c = lane & 3;
+          const uint4 v = *reinterpret_cast<const uint4*>(out_tile + r * 64 + ((c ^ (r >> 1)) & 3) * 16);
+          if (row0 + r < p.M)
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + int64_t(row0 + r) * p.N + n0 + 16 * c) = v;
+        }
+        __syncwarp();
+      } else {
+#pragma unroll
+        for (int pass = 0; pass < (kSwi ? 1 : 2); ++pass) {  // 64 output columns each
+          const int n0 = kSwi ? nb * 128 + 64 * half : nb * kBN + 128 * pass + 64 * half;
+          if (n0 < p.N) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float* a = acc[kSwi ? c : 2 * pass + c];
+              if (p.bias != nullptr) {
+                if (kSwi) {
+                  f8_bias32(a, p.bias + n0 + 32 * c);
+                  f8_bias32(acc[2 + c], p.bias + p.b_row_up + n0 + 32 * c);
+                } else {
+#pragma unroll
+                  for (int g = 0; g < 4; ++g)
+                    if (n0 + 32 * c + 8 * g < p.N) f8_bias8(a + 8 * g, p.bias + n0 + 32 * c + 8 * g);
+                }
+              }
+              if constexpr (kSwi) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) a[i] = __fmul_rn(silu_approx(a[i]), acc[2 + c][i]);
+              }
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                *reinterpret_cast<uint4*>(out_tile + lane * 128 + ((4 * c + g) ^ (lane & 7)) * 16) = f8_pack8(a + 8 * g);
             }
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              ga[i] = __fmul_rn(silu_approx(ga[i]), ua[i]);
-              if constexpr (EPI == kF8SwiGLUQuant) amax = max_nan(amax, fabsf(ga[i]));
+              const int r = 4 * i + (lane >> 3), c = lane & 7;
+              const uint4 v = *reinterpret_cast<const uint4*>(out_tile + r * 128 + (c ^ (r & 7)) * 16);
+              if (row0 + r < p.M && n0 + 8 * c < p.N)
+                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + int64_t(row0 + r) * p.N + n0 + 8 * c) = v;
             }
-            if constexpr (EPI == kF8SwiGLU) {
-              __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out) + int64_t(row) * p.N + n0 + 32 * c + 8 * g;
-              if (row_ok) *reinterpret_cast<uint4*>(out) = f8_pack8(ga);
-            }
-          }
-        if constexpr (EPI == kF8SwiGLUQuant) {
-          // the row's 128 h columns are one scale block; its two halves sit in two warps
-          float* mine = row_max + (iter & 1) * 256 + half * 128 + row_in_cta;
-          *mine = amax;
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&rmax_bar[quarter]);
-          if (!mbar_wait_bounded(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
-          amax = max_nan(amax, row_max[(iter & 1) * 256 + (half ^ 1) * 128 + row_in_cta]);
-          float inv;
-          const float s = fp8_scale(amax, inv);
-          if (row_ok) {
-            uint8_t* out = static_cast<uint8_t*>(p.out) + int64_t(row) * p.N + n0;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              uint32_t w[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float* a = &acc[g >> 1][16 * (g & 1) + 4 * i];
-                w[i] = f32x4_to_e4m3x4(__fmul_rn(a[0], inv), __fmul_rn(a[1], inv), __fmul_rn(a[2], inv),
-                                       __fmul_rn(a[3], inv));
-              }
-              *reinterpret_cast<uint4*>(out + 16 * g) = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            if (half == 0) p.sh[int64_t(nb) * p.M + row] = s;
+            __syncwarp();
           }
         }
       }
     }
+    cp_async_wait_all();
   }
 
   __syncwarp();
   tc_fence_before();
   cluster_sync();
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+  if (warp == kF8Issuer) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
 }  // namespace h3q
