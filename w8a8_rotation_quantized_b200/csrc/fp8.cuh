@@ -214,20 +214,21 @@ __device__ __forceinline__ void f8_bias32(float* acc, const __nv_bfloat16* bias)
 
 enum Fp8Epi : int { kF8BF16 = 0, kF8SwiGLU = 1, kF8SwiGLUQuant = 2 };
 
-constexpr int kF8Stages = 5;
-constexpr int kF8Threads = 384;  // 8 promotion warps, then two producers and two MMA issuers
-constexpr int kF8Producer = 8, kF8Issuer = 10;
+constexpr int kF8Stages = 4;
+constexpr int kF8Warps = 16;                     // promotion warps
+constexpr int kF8Threads = 32 * kF8Warps + 128;  // then operand and scale producers, two MMA issuers
+constexpr int kF8Producer = kF8Warps, kF8Issuer = kF8Warps + 2;
 constexpr int kF8StageBytes = kAStage + kBStage;
-constexpr int kF8ScaleKB = 8;                            // K blocks whose scales are fetched together
-constexpr int kF8ScaleSlot = (kF8ScaleKB * 32 + 32) * 4;  // a warp's 32 rows of them, then two weight blocks' (and padding)
-constexpr int kF8OutTile = 32 * 128;                     // a warp's 32 output rows of 128 bytes
-constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + 8 * kF8OutTile + 8 * 2 * kF8ScaleSlot +
-                           2 * 2 * 128 * 4 /*row maxima*/ + 256 /*barriers*/ + 1024 /*align*/;
+constexpr int kF8ScaleRing = 16;            // K blocks whose scales are in flight or waiting, handed over by fours
+constexpr int kF8ScaleSlot = 128 * 4 + 16;  // a K block's scales of the CTA's 128 rows, then of the two weight blocks
+constexpr int kF8OutTile = 32 * 64;         // a warp's 32 output rows of 64 bytes
+constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + kF8Warps * 2 * kF8OutTile + kF8ScaleRing * kF8ScaleSlot +
+                           2 * 4 * 128 * 4 /*row maxima*/ + 256 /*barriers*/ + 1024 /*align*/;
 static_assert(kF8Smem <= 232448, "shared memory of one CTA");
-// Register split: the launch's 168 per thread, moved from the first warpgroup to
-// the two that hold accumulators.
-constexpr uint32_t kF8RegsCtl = 40, kF8RegsPromote = 232, kF8RegsLaunch = 168;
-static_assert(128 * kF8RegsCtl + 256 * kF8RegsPromote <= kF8Threads * kF8RegsLaunch, "register split");
+// Register split: the launch's 96 per thread, moved from the control warps to the
+// ones that hold accumulators.
+constexpr uint32_t kF8RegsCtl = 32, kF8RegsPromote = 112, kF8RegsLaunch = 96;
+static_assert(128 * kF8RegsCtl + 32 * kF8Warps * kF8RegsPromote <= kF8Threads * kF8RegsLaunch, "register split");
 
 struct Fp8Params {
   int M, N, K;              // N: output columns (SwiGLU: F)
@@ -243,11 +244,16 @@ struct Fp8Params {
   uint64_t wait_limit_ns;
 };
 
-// acc += part * f, 32 columns. One multiply-add per column: the packed two-wide form
-// measured far slower here (1940 against 1280 us for 16384 x 14336 x 5376).
+// acc += part * f, 32 columns, two multiply-adds an instruction: the same rate as
+// single ones, and half the issue slots, which the control warps need.
 __device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&r)[32], float f) {
 #pragma unroll
-  for (int i = 0; i < 32; ++i) acc[i] = __fmaf_rn(__uint_as_float(r[i]), f, acc[i]);
+  for (int i = 0; i < 32; i += 2) {
+    const float2 t = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(f, f),
+                                make_float2(acc[i], acc[i + 1]));
+    acc[i] = t.x;
+    acc[i + 1] = t.y;
+  }
 }
 
 // CTA pairs, 256 x 256 output tiles, TMA ring and cta_group::2 MMAs as in the int8
@@ -261,22 +267,24 @@ __device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&r)
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                    const Fp8Params p) {
+                    const __grid_constant__ CUtensorMap tmOut, const Fp8Params p) {
   constexpr bool kSwi = EPI != kF8BF16;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* sA = smem;
   uint8_t* sB = smem + kF8Stages * kAStage;
-  uint8_t* out_tiles = sB + kF8Stages * kBStage;    // [warp]
-  uint8_t* scale_slots = out_tiles + 8 * kF8OutTile;  // [warp][2]
-  float* row_max = reinterpret_cast<float*>(scale_slots + 8 * 2 * kF8ScaleSlot);  // [tile parity][half][row]
-  uint64_t* full = reinterpret_cast<uint64_t*>(row_max + 2 * 2 * 128);
+  uint8_t* out_tiles = sB + kF8Stages * kBStage;        // [warp][2]
+  uint8_t* scale_ring = out_tiles + kF8Warps * 2 * kF8OutTile;
+  float* row_max = reinterpret_cast<float*>(scale_ring + kF8ScaleRing * kF8ScaleSlot);  // [tile parity][part][row]
+  uint64_t* full = reinterpret_cast<uint64_t*>(row_max + 2 * 4 * 128);
   uint64_t* empty = full + kF8Stages;
   uint64_t* tfull = empty + kF8Stages;
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
-  uint64_t* rmax_bar = drain + 1;  // [quarter]: both halves' row maxima are in shared memory
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(rmax_bar + 4);
+  uint64_t* rmax_bar = drain + 1;  // [quarter]: the four parts' row maxima are in shared memory
+  uint64_t* sfull = rmax_bar + 4;   // [group of four K blocks % 4]: the scales are in shared memory
+  uint64_t* sempty = sfull + 4;     // ... and have been read
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // warp-uniform
@@ -292,16 +300,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 16);  // leader's: 8 promotion warps of each CTA
+      mbar_init(&tempty[b], 2 * kF8Warps);  // leader's: the promotion warps of both CTAs
     }
     mbar_init(drain, 2);  // the two issuers
-    for (int i = 0; i < 4; ++i) mbar_init(&rmax_bar[i], 2);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(&rmax_bar[i], 4);
+      mbar_init(&sfull[i], 32);  // every lane of the scale warp
+      mbar_init(&sempty[i], kF8Warps);
+    }
     *abort_flag = 0;
     fence_mbarrier_init();
   }
   if (warp == kF8Producer && lane == 0) {
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmOut);
   }
   if (warp == kF8Issuer) {
     tmem_alloc_pair(tmem_slot, kTmemCols);
@@ -322,51 +335,78 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     nb = r / gm;
   };
 
-  if (warp >= 8) {
+  if (warp >= kF8Warps) {
     regs_dec<kF8RegsCtl>();
     const int my_tiles = pair < p.num_tiles ? (p.num_tiles - pair + npairs - 1) / npairs : 0;
     const int total = my_tiles * KB;  // K blocks of all of this pair's tiles, in order
-    if (warp < kF8Issuer) {
-      // ------------------------------------------------------------ producers (both CTAs): K blocks of one parity each
+    if (warp == kF8Producer) {
+      // ------------------------------------------------------------ operand tiles (both CTAs)
       const bool one = elect_one();
       const uint64_t pol = policy_evict_last();
-      const int par = warp - kF8Producer;
-      int stage = par;
+      int stage = 0;
       uint32_t phase = 0;
-      int kb = par, tile = pair, a_row = 0, b_row = 0;
-      bool moved = true;
-      int n = par;
-      for (; n < total; n += 2, kb += 2) {
-        while (kb >= KB) {
-          kb -= KB;
-          tile += npairs;
-          moved = true;
-        }
-        if (moved) {
-          int mb, nb;
-          tile_at(tile, mb, nb);
-          a_row = mb * (2 * kBM) + static_cast<int>(rank) * kBM;
-          b_row = kSwi ? (rank == 0 ? nb * 128 : p.b_row_up + nb * 128) : nb * kBN + static_cast<int>(rank) * 128;
-          moved = false;
-        }
-        if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1u, limit, abort_flag)) break;
-        const uint32_t full_leader = cluster_map(&full[stage], 0);
-        if (one) {
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes);
-          tma_load_2d_pair(sA + stage * kAStage, &tmA, full_leader, kb * kBK, a_row, pol);
-          tma_load_2d_pair(sB + stage * kBStage, &tmB, full_leader, kb * kBK, b_row, pol);
-        }
-        stage += 2;
-        if (stage >= kF8Stages) {
-          stage -= kF8Stages;
-          phase ^= 1u;
+      int n = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < p.num_tiles; tile += npairs) {
+        int mb, nb;
+        tile_at(tile, mb, nb);
+        const int a_row = mb * (2 * kBM) + static_cast<int>(rank) * kBM;
+        const int b_row = kSwi ? (rank == 0 ? nb * 128 : p.b_row_up + nb * 128) : nb * kBN + static_cast<int>(rank) * 128;
+        for (int kb = 0; kb < KB; ++kb, ++n) {
+          if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1u, limit, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t full_leader = cluster_map(&full[stage], 0);
+          if (one) {
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes);
+            tma_load_2d_pair(sA + stage * kAStage, &tmA, full_leader, kb * kBK, a_row, pol);
+            tma_load_2d_pair(sB + stage * kBStage, &tmB, full_leader, kb * kBK, b_row, pol);
+          }
+          if (++stage == kF8Stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
         }
       }
-      if (n < total && rank == 0) {
-        // drain this producer's copies that may still be in flight (bounded, ignores abort)
-        for (int m = n - 2; m >= 0 && m > n - 2 - kF8Stages; m -= 2)
+      if (!ok && rank == 0) {
+        // drain the copies that may still be in flight (bounded, ignores abort)
+        for (int m = n - 1; m >= 0 && m >= n - kF8Stages; --m)
           mbar_wait_bounded(&full[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr);
       }
+    } else if (warp == kF8Producer + 1) {
+      // ------------------------------------------------------------ scales (both CTAs)
+      // Up to sixteen K blocks ahead, handed over by fours: each lane copies four rows'
+      // (zeros past the end of M), lanes 0 and 1 the two weight blocks'.
+      int n = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < p.num_tiles; tile += npairs) {
+        int mb, nb;
+        tile_at(tile, mb, nb);
+        const int row = mb * (2 * kBM) + static_cast<int>(rank) * kBM + lane;
+        const float* sx = p.sx + row;
+        const float* sw =
+            p.sw + int64_t(kSwi ? ((lane & 1) ? p.b_row_up / 128 + nb : nb) : min(2 * nb + (lane & 1), p.last_nb)) * KB;
+        for (int kb = 0; kb < KB; ++kb, ++n) {
+          if ((n & 3) == 0 &&
+              !mbar_wait_bounded_warp(&sempty[(n >> 2) & 3], ((n >> 4) & 1) ^ 1u, limit, abort_flag)) {
+            ok = false;
+            break;
+          }
+          const uint32_t dst = smem_u32(scale_ring) + (n & (kF8ScaleRing - 1)) * kF8ScaleSlot + lane * 4;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const bool in = row + 32 * j < p.M;
+            cp_async4(dst + 128 * j, in ? sx + 32 * j : p.sx, in);
+          }
+          if (lane < 2) cp_async4(dst + 512, sw + kb, true);
+          sx += p.M;
+          if ((n & 3) == 3) cp_async_arrive(&sfull[(n >> 2) & 3]);
+        }
+      }
+      if (ok && (n & 3) != 0) cp_async_arrive(&sfull[(n >> 2) & 3]);
+      cp_async_commit();
+      cp_async_wait<0>();
     } else if (rank == 0) {
       // ------------------------------------------------------------ MMA issuers (leader only): one accumulator buffer each
       constexpr uint32_t idesc = idesc_fp8(2 * kBM, kBN);
@@ -402,184 +442,128 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   } else {
     regs_inc<kF8RegsPromote>();
     // -------------------------------------------------------------- promotion and epilogue (both CTAs)
-    // Warps 0..7: warp w owns TMEM lanes 32*(w%4) .. +31 and, of each buffer,
-    // columns [64 half, +64) (chunks 0, 1: gate with SwiGLU) and
-    // [128 + 64 half, +64) (chunks 2, 3: up).
+    // Warps 0..15: warp w owns TMEM lanes 32*(w%4) .. +31 and, of each buffer, columns
+    // [32 part, +32) and [128 + 32 part, +32), part = w/4: with SwiGLU gate and up.
     const int quarter = warp & 3;
-    const int half = warp >> 2;
+    const int part = warp >> 2;
     const int row_in_cta = quarter * 32 + lane;
-    const uint32_t tempty0 = cluster_map(&tempty[0], 0);
-    const uint32_t tempty1 = cluster_map(&tempty[1], 0);
-    const uint32_t tlane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(64 * half);
-    uint8_t* out_tile = out_tiles + warp * kF8OutTile;
-    uint8_t* slots = scale_slots + warp * 2 * kF8ScaleSlot;
-    // Scales of K blocks kb0 .. kb0 + 7 of a tile into a slot, in flight until the slot's
-    // turn comes: each lane its own row's (zero past the end of M or K), lanes 0-15 the
-    // two weight blocks'.
-    auto fetch_scales = [&](int tile, int kb0, int slot) {
-      int mb, nb;
-      tile_at(tile, mb, nb);
-      const int row = mb * (2 * kBM) + static_cast<int>(rank) * kBM + row_in_cta;
-      const uint32_t dst = smem_u32(slots + slot * kF8ScaleSlot);
-      const float* sx = p.sx + int64_t(kb0) * p.M + (row < p.M ? row : 0);
-#pragma unroll
-      for (int j = 0; j < kF8ScaleKB; ++j) {
-        const bool in = kb0 + j < KB;
-        cp_async4(dst + (j * 32 + lane) * 4, in ? sx + int64_t(j) * p.M : p.sx, in && row < p.M);
-      }
-      if (lane < 2 * kF8ScaleKB) {
-        const int j = lane & (kF8ScaleKB - 1), which = lane / kF8ScaleKB;
-        const int nbw = kSwi ? (which ? p.b_row_up / 128 + nb : nb) : min(2 * nb + which, p.last_nb);
-        const bool in = kb0 + j < KB;
-        cp_async4(dst + (kF8ScaleKB * 32 + lane) * 4, in ? p.sw + int64_t(nbw) * KB + kb0 + j : p.sw, in);
-      }
-      cp_async_commit();
-    };
-    int buf = 0;
-    uint32_t buf_phase = 0;
-    int iter = 0, slot = 0;
+    const uint32_t tempty_leader = cluster_map(tempty, 0);
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + static_cast<uint32_t>(32 * part);
+    uint8_t* out_tile = out_tiles + warp * 2 * kF8OutTile;
+    const uint32_t my_scales = smem_u32(scale_ring) + row_in_cta * 4;
+    const uint32_t block_scales = smem_u32(scale_ring) + 512;
+    int n = 0;  // K blocks so far: buffer n % 2, scale slot n % 16
+    int iter = 0;
     bool ok = true;
-    if (pair < p.num_tiles) fetch_scales(pair, 0, 0);
     for (int tile = pair; ok && tile < p.num_tiles; tile += npairs, ++iter) {
-      int mb, nb;
-      tile_at(tile, mb, nb);
-      float acc[4][32];
+      float acc[2][32];
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
+      for (int c = 0; c < 2; ++c)
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
-      for (int kb0 = 0; ok && kb0 < KB; kb0 += kF8ScaleKB) {
-        cp_async_wait_all();
-        __syncwarp();  // this slot is written, and the other one has been read by every lane
-        const float* sc = reinterpret_cast<const float*>(slots + slot * kF8ScaleSlot);
-        slot ^= 1;
-        if (kb0 + kF8ScaleKB < KB)
-          fetch_scales(tile, kb0 + kF8ScaleKB, slot);
-        else if (tile + npairs < p.num_tiles)
-          fetch_scales(tile + npairs, 0, slot);
-        const int nkb = min(kF8ScaleKB, KB - kb0);
 #pragma unroll 1
-        for (int j = 0; j < nkb; ++j) {
-          const float sxv = sc[j * 32 + lane];
-          const float f0 = __fmul_rn(sxv, sc[kF8ScaleKB * 32 + j]);
-          const float f1 = __fmul_rn(sxv, sc[kF8ScaleKB * 33 + j]);
-          if (!mbar_wait_bounded_lazy(&tfull[buf], buf_phase, limit, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          const uint32_t ta = tlane + static_cast<uint32_t>(buf * kBN);
-          uint32_t ra[32], rb[32];
-          tmem_ld32(ta, ra);
-          tmem_ld_wait32(ra);
-          tmem_ld32(ta + 32, rb);
-          f8_promote(acc[0], ra, f0);
-          tmem_ld_wait32(rb);
-          tmem_ld32(ta + 128, ra);
-          f8_promote(acc[1], rb, f0);
-          tmem_ld_wait32(ra);
-          tmem_ld32(ta + 160, rb);
-          f8_promote(acc[2], ra, f1);
-          tmem_ld_wait32(rb);
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(buf == 0 ? tempty0 : tempty1);
-          f8_promote(acc[3], rb, f1);
-          buf ^= 1;
-          if (buf == 0) buf_phase ^= 1u;
+      for (int kb = 0; kb < KB; ++kb, ++n) {
+        if ((n & 3) == 0 && !mbar_wait_bounded_lazy(&sfull[(n >> 2) & 3], (n >> 4) & 1, p.wait_limit_ns, abort_flag)) {
+          ok = false;
+          break;
         }
+        const uint32_t slot = (n & (kF8ScaleRing - 1)) * kF8ScaleSlot;
+        const float sxv = ld_shared_f32(my_scales + slot);
+        const float f0 = __fmul_rn(sxv, ld_shared_f32(block_scales + slot));
+        const float f1 = __fmul_rn(sxv, ld_shared_f32(block_scales + slot + 4));
+        if (!mbar_wait_bounded_lazy(&tfull[n & 1], (n >> 1) & 1, p.wait_limit_ns, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ta = tlane + static_cast<uint32_t>((n & 1) * kBN);
+        uint32_t r[32];
+        tmem_ld32(ta, r);
+        tmem_ld_wait32(r);
+        f8_promote(acc[0], r, f0);
+        tmem_ld32(ta + 128, r);
+        tmem_ld_wait32(r);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_remote(tempty_leader + (n & 1) * 8);
+          if ((n & 3) == 3) mbar_arrive(&sempty[(n >> 2) & 3]);  // every lane has read the group's scales
+        }
+        f8_promote(acc[1], r, f1);
       }
       if (!ok) break;
+      int mb, nb;
+      tile_at(tile, mb, nb);
 
-      // Epilogue: the warp's 32 rows go through its shared-memory tile, 128 bytes a row
-      // with 16-byte chunks swizzled by the row, and leave as whole lines.
+      // Epilogue: 32 rows x 32 columns at a time through one of the warp's two
+      // shared-memory tiles (in TMA's swizzle), which a TMA store takes away while the
+      // next tile's K blocks are promoted.
       const int row0 = mb * (2 * kBM) + static_cast<int>(rank) * kBM + quarter * 32;
-      if constexpr (EPI == kF8SwiGLUQuant) {
-        const int n0 = nb * 128 + 64 * half;  // first h column of this thread
+      bulk_wait_read<0>();  // lane 0's earlier stores have read their tiles
+      __syncwarp();
+      if constexpr (kSwi) {
+        const int n0 = nb * 128 + 32 * part;  // first h column of this thread
         float amax = 0.0f;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          if (p.bias != nullptr) {
-            f8_bias32(acc[c], p.bias + n0 + 32 * c);
-            f8_bias32(acc[2 + c], p.bias + p.b_row_up + n0 + 32 * c);
-          }
-#pragma unroll
-          for (int i = 0; i < 32; ++i) {
-            acc[c][i] = __fmul_rn(silu_approx(acc[c][i]), acc[2 + c][i]);
-            amax = max_nan(amax, fabsf(acc[c][i]));
-          }
+        if (p.bias != nullptr) {
+          f8_bias32(acc[0], p.bias + n0);
+          f8_bias32(acc[1], p.bias + p.b_row_up + n0);
         }
-        // the row's 128 h columns are one scale block; its two halves sit in two warps
-        float* maxima = row_max + (iter & 1) * 256;
-        maxima[half * 128 + row_in_cta] = amax;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&rmax_bar[quarter]);
-        if (!mbar_wait_bounded_lazy(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
-        amax = max_nan(amax, maxima[(half ^ 1) * 128 + row_in_cta]);
-        float inv;
-        const float s = fp8_scale(amax, inv);
-        if (half == 0 && row0 + lane < p.M) p.sh[int64_t(nb) * p.M + row0 + lane] = s;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {  // 64 bytes a row, two rows to a 128-byte line
-          uint32_t w[4];
+        for (int i = 0; i < 32; ++i) {
+          acc[0][i] = __fmul_rn(silu_approx(acc[0][i]), acc[1][i]);
+          if constexpr (EPI == kF8SwiGLUQuant) amax = max_nan(amax, fabsf(acc[0][i]));
+        }
+        if constexpr (EPI == kF8SwiGLUQuant) {
+          // the row's 128 h columns are one scale block; its four parts sit in four warps
+          float* maxima = row_max + (iter & 1) * 512 + row_in_cta;
+          maxima[part * 128] = amax;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&rmax_bar[quarter]);
+          if (!mbar_wait_bounded_lazy(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* a = &acc[g >> 1][16 * (g & 1) + 4 * i];
-            w[i] = f32x4_to_e4m3x4(__fmul_rn(a[0], inv), __fmul_rn(a[1], inv), __fmul_rn(a[2], inv),
-                                   __fmul_rn(a[3], inv));
+          for (int i = 0; i < 4; ++i) amax = max_nan(amax, maxima[i * 128]);
+          float inv;
+          const float s = fp8_scale(amax, inv);
+          if (part == 0 && row0 + lane < p.M) p.sh[int64_t(nb) * p.M + row0 + lane] = s;
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {  // 32 bytes a row, four rows to a 128-byte line
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* a = &acc[0][16 * g + 4 * i];
+              w[i] = f32x4_to_e4m3x4(__fmul_rn(a[0], inv), __fmul_rn(a[1], inv), __fmul_rn(a[2], inv),
+                                     __fmul_rn(a[3], inv));
+            }
+            *reinterpret_cast<uint4*>(out_tile + lane * 32 + ((g ^ (lane >> 2)) & 1) * 16) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
-          *reinterpret_cast<uint4*>(out_tile + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) =
-              make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 2), c = lane & 3;
-          const uint4 v = *reinterpret_cast<const uint4*>(out_tile + r * 64 + ((c ^ (r >> 1)) & 3) * 16);
-          if (row0 + r < p.M)
-            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.out) + int64_t(row0 + r) * p.N + n0 + 16 * c) = v;
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<uint4*>(out_tile + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) = f8_pack8(&acc[0][8 * g]);
         }
+        fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0 && row0 < p.M) tma_store_2d(&tmOut, out_tile, n0, row0);
       } else {
 #pragma unroll
-        for (int pass = 0; pass < (kSwi ? 1 : 2); ++pass) {  // 64 output columns each
-          const int n0 = kSwi ? nb * 128 + 64 * half : nb * kBN + 128 * pass + 64 * half;
+        for (int pass = 0; pass < 2; ++pass) {
+          const int n0 = nb * kBN + 128 * pass + 32 * part;
           if (n0 < p.N) {
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float* a = acc[kSwi ? c : 2 * pass + c];
-              if (p.bias != nullptr) {
-                if (kSwi) {
-                  f8_bias32(a, p.bias + n0 + 32 * c);
-                  f8_bias32(acc[2 + c], p.bias + p.b_row_up + n0 + 32 * c);
-                } else {
-#pragma unroll
-                  for (int g = 0; g < 4; ++g)
-                    if (n0 + 32 * c + 8 * g < p.N) f8_bias8(a + 8 * g, p.bias + n0 + 32 * c + 8 * g);
-                }
-              }
-              if constexpr (kSwi) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) a[i] = __fmul_rn(silu_approx(a[i]), acc[2 + c][i]);
-              }
-#pragma unroll
-              for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<uint4*>(out_tile + lane * 128 + ((4 * c + g) ^ (lane & 7)) * 16) = f8_pack8(a + 8 * g);
+            for (int g = 0; g < 4; ++g) {
+              if (p.bias != nullptr && n0 + 8 * g < p.N) f8_bias8(&acc[pass][8 * g], p.bias + n0 + 8 * g);
+              *reinterpret_cast<uint4*>(out_tile + pass * kF8OutTile + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) =
+                  f8_pack8(&acc[pass][8 * g]);
             }
+            fence_proxy_async_smem();
             __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int r = 4 * i + (lane >> 3), c = lane & 7;
-              const uint4 v = *reinterpret_cast<const uint4*>(out_tile + r * 128 + (c ^ (r & 7)) * 16);
-              if (row0 + r < p.M && n0 + 8 * c < p.N)
-                *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + int64_t(row0 + r) * p.N + n0 + 8 * c) = v;
-            }
-            __syncwarp();
+            if (lane == 0 && row0 < p.M) tma_store_2d(&tmOut, out_tile + pass * kF8OutTile, n0, row0);
           }
         }
       }
     }
-    cp_async_wait_all();
+    bulk_wait_read<0>();
   }
 
   __syncwarp();

@@ -188,12 +188,28 @@ h3q_status launch_gemm_fp4(const uint8_t* a, const uint8_t* a_sf, const float* a
   return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
 
+// The fp8 product's output, bf16 or one byte an element: boxes of 32 columns x 32 rows,
+// swizzled over the box's row.
+bool make_tmap_f8_out(CUtensorMap* map, void* base, int64_t rows, int64_t cols, bool bytes) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols * (bytes ? 1 : 2))};
+  const cuuint32_t box[2] = {32, 32};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, bytes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, base, dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, bytes ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
+             CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int EPI>
 h3q_status launch_gemm_fp8(const uint8_t* a, const float* sx, int64_t M, int64_t K, const uint8_t* b, const float* sw,
                            int64_t b_rows, int64_t N_out, const void* bias, void* out, float* sh,
                            cudaStream_t stream) {
-  CUtensorMap ta, tb;
-  if (!make_tmap_i8(&ta, a, M, K) || !make_tmap_i8(&tb, b, b_rows, K)) return H3Q_ERR_CUDA;
+  CUtensorMap ta, tb, tout;
+  if (!make_tmap_i8(&ta, a, M, K) || !make_tmap_i8(&tb, b, b_rows, K) ||
+      !make_tmap_f8_out(&tout, out, M, N_out, EPI == h3q::kF8SwiGLUQuant))
+    return H3Q_ERR_CUDA;
   const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_kernel<EPI>);
   if (ensure_smem_attr(kernel, static_cast<int>(h3q::kF8Smem)) != cudaSuccess) return H3Q_ERR_CUDA;
   // the kernel's register split assumes this many registers per thread at launch
@@ -225,7 +241,7 @@ h3q_status launch_gemm_fp8(const uint8_t* a, const float* sx, int64_t M, int64_t
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
-  h3q::gemm_fp8_kernel<EPI><<<2 * pairs, h3q::kF8Threads, h3q::kF8Smem, stream>>>(ta, tb, p);
+  h3q::gemm_fp8_kernel<EPI><<<2 * pairs, h3q::kF8Threads, h3q::kF8Smem, stream>>>(ta, tb, tout, p);
   return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
 

@@ -57,13 +57,9 @@ constexpr int kLoraRing = H3Q_LORA_RING;  // A_rot rows in flight per thread (a 
 static_assert((kLoraRing & (kLoraRing - 1)) == 0, "ring depth must be a power of two");
 
 // 16-byte global -> shared copy through L2 only (the per-thread async copy of
-// sm_80 and later), its commit and its bounded-depth wait.
+// sm_80 and later).
 __device__ __forceinline__ void cp_async_16(void* smem_dst, const void* gsrc) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(smem_dst)), "l"(gsrc) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t cluster_addr) {
