@@ -87,33 +87,91 @@ __device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float inv) {
   return make_uint2(f32x4_to_e4m3x4(t[0], t[1], t[2], t[3]), f32x4_to_e4m3x4(t[4], t[5], t[6], t[7]));
 }
 
-// 1 x 128 blocks: sixteen lanes per block, eight elements each.
+// Eight consecutive elements as loaded, the largest magnitude among them, and their
+// codes. bf16 magnitudes compare as packed pairs; a NaN wins.
 template <typename T>
-__global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__ x, int64_t M, int K, int KB,
-                                                           uint8_t* __restrict__ codes, float* __restrict__ sx) {
-  const int64_t total = M * KB;
-  const int l = threadIdx.x & 15;
-  const int64_t first = (int64_t(blockIdx.x) * blockDim.x + threadIdx.x) >> 4;
-  const int64_t step = (int64_t(gridDim.x) * blockDim.x) >> 4;
-  const int64_t rounds = (total + step - 1) / step;
-  for (int64_t it = 0; it < rounds; ++it) {  // every lane runs every round: the shuffles need them all
-    const int64_t b = first + it * step;
-    const int64_t m = b / KB;
-    const int kb = static_cast<int>(b - m * KB);
-    const int col = kb * 128 + 8 * l;
-    const bool ok = b < total && col < K;
-    float v[8] = {};
-    if (ok) fp8_load8(x + m * K + col, v);
+struct Fp8Chunk;
+
+template <>
+struct Fp8Chunk<__nv_bfloat16> {
+  uint32_t w[4] = {0u, 0u, 0u, 0u};
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
+  }
+  __device__ __forceinline__ float absmax16() const {  // over the sixteen lanes that share a block
+    auto two = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
+    __nv_bfloat162 m = two(w[0] & 0x7FFF7FFFu);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, two(w[i] & 0x7FFF7FFFu));
+    uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) {
+      m = __hmax2_nan(two(u), two(__shfl_xor_sync(0xFFFFFFFFu, u, o)));
+      u = *reinterpret_cast<const uint32_t*>(&m);
+    }
+    return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ uint2 codes(float inv) const {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+    return fp8_codes8(v, inv);
+  }
+};
+
+template <>
+struct Fp8Chunk<float> {
+  float v[8] = {};
+  __device__ __forceinline__ void load(const float* p) {
+    const float4 a = __ldcs(reinterpret_cast<const float4*>(p)), b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  }
+  __device__ __forceinline__ float absmax16() const {
     float a = fp8_absmax8(v);
 #pragma unroll
     for (int o = 1; o < 16; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    float inv;
-    const float s = fp8_scale(a, inv);
-    if (ok) {
-      *reinterpret_cast<uint2*>(codes + m * K + col) = fp8_codes8(v, inv);
-      if (l == 0) sx[int64_t(kb) * M + m] = s;
-    }
+    return a;
   }
+  __device__ __forceinline__ uint2 codes(float inv) const { return fp8_codes8(v, inv); }
+};
+
+// 1 x 128 blocks. A CTA takes 32 rows x 256 columns, a warp four of the rows: sixteen
+// lanes a block, eight elements each, all four loads in flight at once. The scales of
+// the 32 rows leave together, a line for each of the two K blocks. Bound by memory
+// (264 MB for 16384 x 5376 bf16).
+constexpr int kF8QuantRows = 32;
+
+template <typename T>
+__global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__ x, int64_t M, int K, int KB,
+                                                           uint8_t* __restrict__ codes, float* __restrict__ sx) {
+  __shared__ float scales[2][kF8QuantRows];
+  const int pairs = (KB + 1) >> 1;
+  const int rb = blockIdx.x / pairs;
+  const int kb = 2 * (blockIdx.x - rb * pairs);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int col = kb * 128 + 8 * lane;
+  const int64_t m0 = int64_t(rb) * kF8QuantRows;
+  Fp8Chunk<T> v[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = m0 + 4 * warp + i;
+    if (m < M && col < K) v[i].load(x + m * K + col);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t m = m0 + 4 * warp + i;
+    float inv;
+    const float s = fp8_scale(v[i].absmax16(), inv);
+    if (m < M && col < K) *reinterpret_cast<uint2*>(codes + m * K + col) = v[i].codes(inv);
+    if ((lane & 15) == 0) scales[lane >> 4][4 * warp + i] = s;
+  }
+  __syncthreads();
+  if (warp < 2 && kb + warp < KB && m0 + lane < M) sx[int64_t(kb + warp) * M + m0 + lane] = scales[warp][lane];
 }
 
 // 128 x 128 blocks: one CTA of 256 threads per block; thread t holds the

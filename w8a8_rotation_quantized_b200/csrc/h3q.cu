@@ -245,12 +245,21 @@ h3q_status launch_gemm_fp8(const uint8_t* a, const float* sx, int64_t M, int64_t
   return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
 
+// Warps of qk_norm_rope wanted per SM: below that many tokens an SM, the heads of a
+// token are split over several warps.
+constexpr int kQkWarpsPerSm = 16;
+
 template <int G>
-void launch_qk(const h3q::QkParams& p, bool interleaved, unsigned grid, cudaStream_t stream) {
+void launch_qk(const h3q::QkParams& p, bool interleaved, int sms, cudaStream_t stream) {
+  const int64_t steps = (p.Hq + 32 / G - 1) / (32 / G) + (p.Hk + 32 / G - 1) / (32 / G);
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(steps, 65535), int64_t(sms) * kQkWarpsPerSm / p.S));
+  const unsigned warps = static_cast<unsigned>(std::min<int64_t>(8, p.S));
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((p.S + warps - 1) / warps, int64_t(sms) * 8)),
+                  static_cast<unsigned>(parts));
   if (interleaved)
-    h3q::qk_norm_rope_kernel<G, true><<<grid, 256, 0, stream>>>(p);
+    h3q::qk_norm_rope_kernel<G, true><<<grid, 32 * warps, 0, stream>>>(p);
   else
-    h3q::qk_norm_rope_kernel<G, false><<<grid, 256, 0, stream>>>(p);
+    h3q::qk_norm_rope_kernel<G, false><<<grid, 32 * warps, 0, stream>>>(p);
 }
 
 // [rows, cols] bf16 row-major, boxes of 64 columns (128 bytes) x 128 rows,
@@ -554,9 +563,9 @@ static h3q_status fp8_quantize_any(bool weight, const void* x, int x_dtype, int6
     else
       h3q::fp8_weight_kernel<float><<<g, 256, 0, stream>>>(xf, rows, k, KB, codes, scales);
   } else {
-    const int sms = sm_count();
-    if (sms <= 0) return H3Q_ERR_CUDA;
-    const unsigned g = static_cast<unsigned>(std::min<int64_t>((rows * KB + 15) / 16, int64_t(sms) * 8));
+    const int64_t blocks = (rows + h3q::kF8QuantRows - 1) / h3q::kF8QuantRows * ((KB + 1) / 2);
+    if (blocks > INT32_MAX) return H3Q_ERR_UNSUPPORTED;
+    const unsigned g = static_cast<unsigned>(blocks);
     if (x_dtype == H3Q_DTYPE_BF16)
       h3q::fp8_quantize_kernel<__nv_bfloat16><<<g, 256, 0, stream>>>(xb, rows, k, KB, codes, scales);
     else
@@ -649,12 +658,11 @@ h3q_status h3q_qk_norm_rope(const void* q, const void* k, int64_t S, int64_t Hq,
   p.eps = eps;
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>((S + 7) / 8, int64_t(sms) * 8));
   const bool il = interleaved != 0;
-  if (D <= 32) launch_qk<4>(p, il, grid, stream);
-  else if (D <= 64) launch_qk<8>(p, il, grid, stream);
-  else if (D <= 128) launch_qk<16>(p, il, grid, stream);
-  else launch_qk<32>(p, il, grid, stream);
+  if (D <= 32) launch_qk<4>(p, il, sms, stream);
+  else if (D <= 64) launch_qk<8>(p, il, sms, stream);
+  else if (D <= 128) launch_qk<16>(p, il, sms, stream);
+  else launch_qk<32>(p, il, sms, stream);
   return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
 

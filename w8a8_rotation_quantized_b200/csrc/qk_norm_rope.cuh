@@ -6,7 +6,13 @@
 // normalised. Rounded to bf16 once, at the end.
 //
 // A head is read by a group of lanes, eight elements (16 bytes) each; a warp works on
-// one token, so its lanes load the token's table row once for all of its heads.
+// one token at a time, so its lanes load the token's table row once for all of its
+// heads and fold the norm's weights into it: with C_i = w_i c_i and S_i = -+w_p s_i (p
+// the partner of i), the result is r (x_i C_i + x_p S_i), three operations an element.
+// Four heads a lane group are in flight at once. The kernel reads and writes every
+// element once and is bound by memory: 84 heads of 128 over 16384 tokens take 704 MB.
+// Few tokens are spread over more warps by splitting the heads.
+//
 // Each lane holds its elements until they are stored, and a group's loads come
 // before its stores, so q_out and k_out may be q and k themselves.
 #pragma once
@@ -28,80 +34,132 @@ struct QkParams {
   float eps;
 };
 
-// G: lanes per head (a power of two, 8 G >= D).
+// Eight fp32 from eight consecutive bf16.
+__device__ __forceinline__ void qk_load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
+
+// G: lanes per head (a power of two, 8 G >= D). Grid: x tokens (warps stride over
+// them), y the part of the heads.
 template <int G, bool INTER>
 __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
-  constexpr int kHeads = 32 / G;  // heads a warp takes at once
+  constexpr int kHeads = 32 / G;  // heads a warp step takes
+  constexpr int kUnroll = 4;      // steps in flight
   const int lane = threadIdx.x & 31;
   const int l = lane % G, sub = lane / G;
-  const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
   const bool live = 8 * l < p.D;
   const bool turns = 8 * l < p.rot;
   const int half = p.rot >> 1;
-  const int H = p.Hq + p.Hk;
   // half-split pairs: element i's partner sits rot / 2 away, in another lane
   const bool second = !INTER && 8 * l >= half;
-  const int partner = INTER ? lane : (turns ? (second ? lane - half / 8 : lane + half / 8) : lane);
-  const int pl = partner % G;
+  const int partner = INTER || !turns ? lane : (second ? lane - half / 8 : lane + half / 8);
+  const float inv_d = __frcp_rn(static_cast<float>(p.D));
+  const int steps_q = (p.Hq + kHeads - 1) / kHeads, steps_k = (p.Hk + kHeads - 1) / kHeads;
+  const int per = (steps_q + steps_k + gridDim.y - 1) / gridDim.y;
+  const int begin = blockIdx.y * per, end = min(begin + per, steps_q + steps_k);
+  const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
   for (int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); t < p.S; t += warps) {
-    float c[8], s[8];
+    float c[8], s[8];  // this token's table row for this lane's elements, s signed
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = 1.0f, s[i] = 0.0f;
     if (turns) {
       const int at = p.pos != nullptr ? p.pos[t] : static_cast<int>(t);
       const bool good = at >= 0 && at < p.P;
-      const int64_t off = int64_t(good ? at : 0) * half;
+      const int64_t off = int64_t(good ? at : 0) * half + (INTER ? 4 * l : 8 * l - (second ? half : 0));
+      constexpr int kVec = INTER ? 1 : 2;  // 16-byte pieces of the row
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int j = INTER ? 4 * l + i / 2 : (8 * l + i) - (second ? half : 0);
-        c[i] = good ? __ldg(p.cos + off + j) : __int_as_float(0x7FC00000);
-        s[i] = __ldg(p.sin + off + j);
-        if (INTER ? !(i & 1) : !second) s[i] = -s[i];  // the pair's first element takes - b s
-      }
-    }
-    for (int h0 = 0; h0 < H; h0 += kHeads) {
-      const int h = h0 + sub;
-      const bool is_q = h < p.Hq;
-      const bool ok = live && h < H;
-      const int64_t hc = int64_t(is_q ? h : h - p.Hq) * p.D + 8 * l;
-      uint4 raw = make_uint4(0u, 0u, 0u, 0u);
-      if (ok) raw = *reinterpret_cast<const uint4*>((is_q ? p.q + t * p.ldq : p.k + t * p.ldk) + hc);
-      const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-      float x[8], xp[8];
-      float ss = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        ss = __fmaf_rn(x[2 * i], x[2 * i], ss);
-        ss = __fmaf_rn(x[2 * i + 1], x[2 * i + 1], ss);
-        const uint32_t o = INTER ? w[i] : __shfl_sync(0xFFFFFFFFu, w[i], partner);
-        xp[2 * i] = __uint_as_float(INTER ? o & 0xFFFF0000u : o << 16);
-        xp[2 * i + 1] = __uint_as_float(INTER ? o << 16 : o & 0xFFFF0000u);
-      }
-#pragma unroll
-      for (int o = 1; o < G; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-      const float r = __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(ss, static_cast<float>(p.D)), p.eps)));
-      if (ok) {
-        const __nv_bfloat16* wt = is_q ? p.wq : p.wk;
-        uint32_t out[4];
-        float y[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float n = __fmul_rn(x[i], r);
-          if (wt != nullptr) n = __fmul_rn(n, __bfloat162float(wt[8 * l + i]));
-          if (turns) {
-            float np = __fmul_rn(xp[i], r);
-            if (wt != nullptr) np = __fmul_rn(np, __bfloat162float(wt[INTER ? 8 * l + (i ^ 1) : 8 * pl + i]));
-            n = __fmaf_rn(n, c[i], __fmul_rn(np, s[i]));
-          }
-          y[i] = n;
-        }
+      for (int v = 0; v < kVec; ++v) {
+        const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + off) + v);
+        const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + off) + v);
+        const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-          out[i] = *reinterpret_cast<const uint32_t*>(&b);
+          if (INTER) {
+            c[2 * i] = c[2 * i + 1] = cc[i];
+            s[2 * i] = -ss[i];
+            s[2 * i + 1] = ss[i];
+          } else {
+            c[4 * v + i] = cc[i];
+            s[4 * v + i] = second ? ss[i] : -ss[i];
+          }
         }
-        *reinterpret_cast<uint4*>((is_q ? p.qo + t * p.ldqo : p.ko + t * p.ldko) + hc) =
-            make_uint4(out[0], out[1], out[2], out[3]);
+      }
+      if (!good) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = __int_as_float(0x7FC00000);
+      }
+    }
+#pragma unroll 1
+    for (int which = 0; which < 2; ++which) {
+      const int base = which ? steps_q : 0;
+      const int lo = max(begin, base) - base, hi = min(end, base + (which ? steps_k : steps_q)) - base;
+      if (lo >= hi) continue;
+      const int H = which ? p.Hk : p.Hq;
+      const __nv_bfloat16* wt = which ? p.wk : p.wq;
+      const __nv_bfloat16* src = (which ? p.k + t * p.ldk : p.q + t * p.ldq) + 8 * l;
+      __nv_bfloat16* dst = (which ? p.ko + t * p.ldko : p.qo + t * p.ldqo) + 8 * l;
+      float cw[8], sw[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) cw[i] = c[i], sw[i] = s[i];
+      if (wt != nullptr && live) {
+        float wi[8], wp[8];
+        qk_load8(wt + 8 * l, wi);
+        qk_load8(wt + 8 * (partner % G), wp);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          cw[i] = __fmul_rn(c[i], wi[i]);
+          sw[i] = __fmul_rn(s[i], INTER ? wp[i ^ 1] : wp[i]);
+        }
+      }
+      for (int st = lo; st < hi; st += kUnroll) {
+        uint4 raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          const int h = (st + u) * kHeads + sub;
+          raw[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (st + u < hi && live && h < H) raw[u] = *reinterpret_cast<const uint4*>(src + int64_t(h) * p.D);
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+          if (st + u >= hi) break;  // the same for the whole warp
+          const int h = (st + u) * kHeads + sub;
+          const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+          float x[8], y[8];
+          float ss = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            ss = __fmaf_rn(x[2 * i], x[2 * i], ss);
+            ss = __fmaf_rn(x[2 * i + 1], x[2 * i + 1], ss);
+          }
+#pragma unroll
+          for (int o = 1; o < G; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+          const float r = rsqrtf(__fmaf_rn(ss, inv_d, p.eps));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t o = INTER ? w[i] : __shfl_sync(0xFFFFFFFFu, w[i], partner);
+            const float p0 = __uint_as_float(INTER ? o & 0xFFFF0000u : o << 16);
+            const float p1 = __uint_as_float(INTER ? o << 16 : o & 0xFFFF0000u);
+            y[2 * i] = __fmul_rn(__fmaf_rn(x[2 * i], cw[2 * i], __fmul_rn(p0, sw[2 * i])), r);
+            y[2 * i + 1] = __fmul_rn(__fmaf_rn(x[2 * i + 1], cw[2 * i + 1], __fmul_rn(p1, sw[2 * i + 1])), r);
+          }
+          if (live && h < H) {
+            uint32_t out[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+              out[i] = *reinterpret_cast<const uint32_t*>(&b);
+            }
+            *reinterpret_cast<uint4*>(dst + int64_t(h) * p.D) = make_uint4(out[0], out[1], out[2], out[3]);
+          }
+        }
       }
     }
   }
