@@ -631,4 +631,326 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   if (warp == kF8Issuer) tmem_dealloc_pair(tmem, kTmemCols);
 }
 
+// ---------------------------------------------------------------- product, few tokens
+// With few tokens the product is bound by reading the weight, so the weight is the
+// MMA's M side: a CTA takes 128 weight rows (SwiGLU: 128 gate and the 128 matching up
+// rows) and TM tokens (the N side), and where the row tiles do not fill the SMs a
+// cluster of C CTAs splits the K axis of one tile. Every K block of 128 is summed into
+// a tensor-memory buffer of its own and promoted into fp32 registers with its scales as
+// in the large kernel (thread = weight row, register = token). The CTAs of a cluster
+// then leave their partial sums in shared memory, and each adds up, in the order of the
+// K axis, the tokens that fall to it and writes them out (a warp per token, four
+// columns a lane), so the result does not depend on timing and nothing is kept in
+// global memory.
+constexpr int kF8sMaxStages = 12;
+constexpr int kF8sThreads = 256;  // four promotion warps, operands, MMA, scales, one idle until the output
+constexpr int kF8sScaleRing = 16;
+
+template <int R, int TM>
+struct Fp8Small {
+  static constexpr int kStage = R * 128 * 128 + TM * 128;
+  static constexpr int kCols = R * TM;                       // tensor-memory columns of one K block
+  static constexpr int kBufs = kCols >= 256 ? 2 : 4;
+  static constexpr int kTmem = kCols * kBufs < 32 ? 32 : kCols * kBufs;
+  static constexpr int kPartials = R * TM * 128 * 4;
+  static_assert(kPartials <= 2 * kStage, "the partial sums fit in the operand ring");
+  static constexpr int kScaleSlot = TM * 4 + 16;
+  static constexpr int kFixed = kF8sScaleRing * kScaleSlot + 512 /*barriers*/ + 1024 /*align*/;
+};
+
+struct Fp8SmallParams {
+  int M, N, KB;
+  int num_m, num_n;    // token tiles, row tiles
+  int stages, splits;  // ring depth; CTAs per cluster
+  int up_row;          // SwiGLU: first up row of the weight (= F)
+  int swiglu_rows;     // F / 128
+  const float *sx, *sw;
+  const __nv_bfloat16* bias;
+  void* out;
+  float* sh;
+  uint64_t wait_limit_ns;
+};
+
+// D[tmem] (+)= A[smem] * B[smem]^T, e4m3 x e4m3 -> fp32, one CTA.
+__device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                        uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
+                 "+r"(r[15])::"memory");
+}
+
+__device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(cluster_addr)
+               : "memory");
+  return v;
+}
+
+__device__ __forceinline__ float4 ld_shared_f32x4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+
+template <int EPI, int TM>
+__global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <= 64 ? 2 : 1)
+    gemm_fp8_small_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                          const Fp8SmallParams p) {
+  constexpr int R = EPI == kF8BF16 ? 1 : 2;
+  using Cfg = Fp8Small<R, TM>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int S = p.stages;
+  uint8_t* ring = smem;  // [stage]: R weight tiles, then the token tile
+  uint8_t* scale_ring = ring + S * Cfg::kStage;
+  uint64_t* full = reinterpret_cast<uint64_t*>(scale_ring + kF8sScaleRing * Cfg::kScaleSlot);
+  uint64_t* empty = full + kF8sMaxStages;
+  uint64_t* tfull = empty + kF8sMaxStages;
+  uint64_t* tempty = tfull + 4;
+  uint64_t* sfull = tempty + 4;  // [group of four K blocks % 4]
+  uint64_t* sempty = sfull + 4;
+  uint64_t* drain = sempty + 4;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const int rank = blockIdx.x % p.splits;
+  const int tile = blockIdx.x / p.splits;
+  const int nt = tile / p.num_m, mt = tile - nt * p.num_m;
+  const int kb0 = static_cast<int>(int64_t(p.KB) * rank / p.splits);
+  const int nkb = static_cast<int>(int64_t(p.KB) * (rank + 1) / p.splits) - kb0;
+  const uint64_t limit = p.wait_limit_ns;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < S; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 4; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 4);
+      mbar_init(&sfull[b], 32);
+      mbar_init(&sempty[b], 4);
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    fence_mbarrier_init();
+  }
+  if (warp == 4 && lane == 0) {
+    tma_prefetch_desc(&tmW);
+    tma_prefetch_desc(&tmX);
+  }
+  if (warp == 5) {
+    tmem_alloc(tmem_slot, Cfg::kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+
+  if (warp == 4) {
+    // ------------------------------------------------------------ operand tiles
+    const bool one = elect_one();
+    const uint64_t pol = policy_evict_normal();
+    int stage = 0, i = 0;
+    uint32_t phase = 0;
+    for (; i < nkb; ++i) {
+      if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1u, limit, abort_flag)) break;
+      if (one) {
+        uint8_t* dst = ring + stage * Cfg::kStage;
+        const int k = (kb0 + i) * 128;
+        mbar_arrive_expect_tx(&full[stage], Cfg::kStage);
+        tma_load_2d(dst, &tmW, &full[stage], k, nt * 128, pol);
+        if (R == 2) tma_load_2d(dst + 128 * 128, &tmW, &full[stage], k, p.up_row + nt * 128, pol);
+        tma_load_2d(dst + R * 128 * 128, &tmX, &full[stage], k, mt * TM, pol);
+      }
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    // past a wait that ran out: the copies still in flight (bounded, ignores abort)
+    if (i < nkb)
+      for (int m = i - 1; m >= 0 && m >= i - S; --m)
+        mbar_wait_bounded(&full[m % S], static_cast<uint32_t>((m / S) & 1), limit, nullptr);
+  } else if (warp == 5) {
+    // ------------------------------------------------------------ MMA issuer
+    constexpr uint32_t idesc = idesc_fp8(128, TM);
+    const bool one = elect_one();
+    int stage = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < nkb; ++i) {
+      const int b = i % Cfg::kBufs;
+      if (!mbar_wait_bounded_warp(&full[stage], phase, limit, abort_flag) ||
+          !mbar_wait_bounded_warp(&tempty[b], ((i / Cfg::kBufs) & 1) ^ 1u, limit, abort_flag))
+        break;
+      tc_fence_after();
+      const uint32_t base = smem_u32(ring + stage * Cfg::kStage);
+      const uint64_t xd = smem_desc_sw128(base + R * 128 * 128);
+      if (one) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const uint64_t wd = smem_desc_sw128(base + r * 128 * 128);
+          const uint32_t d = tmem + static_cast<uint32_t>(b * Cfg::kCols + r * TM);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) mma_fp8(d, wd + 2u * k, xd + 2u * k, idesc, k != 0 ? 1u : 0u);
+        }
+        mma_commit(&tfull[b]);
+        mma_commit(&empty[stage]);
+      }
+      if (++stage == S) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+    if (one) mma_commit(drain);
+    mbar_wait_bounded(drain, 0, limit, nullptr);
+  } else if (warp == 6) {
+    // ------------------------------------------------------------ scales, handed over by fours
+    bool ok = true;
+    for (int i = 0; ok && i < nkb; ++i) {
+      if ((i & 3) == 0 && !mbar_wait_bounded_warp(&sempty[(i >> 2) & 3], ((i >> 4) & 1) ^ 1u, limit, abort_flag)) {
+        ok = false;
+        break;
+      }
+      const uint32_t dst = smem_u32(scale_ring) + (i & (kF8sScaleRing - 1)) * Cfg::kScaleSlot;
+      const int64_t kb = kb0 + i;
+#pragma unroll
+      for (int j = 0; j < (TM + 31) / 32; ++j) {
+        const int m = 32 * j + lane;
+        const bool in = mt * TM + m < p.M;
+        if (m < TM) cp_async4(dst + m * 4, in ? p.sx + kb * p.M + mt * TM + m : p.sx, in);
+      }
+      if (lane < R) cp_async4(dst + TM * 4 + lane * 4, p.sw + int64_t(nt + lane * p.swiglu_rows) * p.KB + kb, true);
+      if ((i & 3) == 3 || i == nkb - 1) cp_async_arrive(&sfull[(i >> 2) & 3]);
+    }
+    cp_async_commit();
+    cp_async_wait<0>();
+  } else if (warp < 4) {
+    // ------------------------------------------------------------ promotion: thread = weight row
+    float acc[R][TM];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int m = 0; m < TM; ++m) acc[r][m] = 0.0f;
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+#pragma unroll 1
+    for (int i = 0; i < nkb; ++i) {
+      const int b = i % Cfg::kBufs;
+      if ((i & 3) == 0 && !mbar_wait_bounded_lazy(&sfull[(i >> 2) & 3], (i >> 4) & 1, limit, abort_flag)) break;
+      if (!mbar_wait_bounded_lazy(&tfull[b], (i / Cfg::kBufs) & 1, limit, abort_flag)) break;
+      tc_fence_after();
+      const uint32_t slot = smem_u32(scale_ring) + (i & (kF8sScaleRing - 1)) * Cfg::kScaleSlot;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float swv = ld_shared_f32(slot + TM * 4 + r * 4);
+#pragma unroll
+        for (int c = 0; c < TM / 16; ++c) {
+          uint32_t v[16];
+          tmem_ld16(tlane + static_cast<uint32_t>(b * Cfg::kCols + r * TM + 16 * c), v);
+          tmem_ld_wait16(v);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float4 s = ld_shared_f32x4(slot + (16 * c + 4 * q) * 4);
+            float* a = &acc[r][16 * c + 4 * q];
+            a[0] = __fmaf_rn(__uint_as_float(v[4 * q]), __fmul_rn(s.x, swv), a[0]);
+            a[1] = __fmaf_rn(__uint_as_float(v[4 * q + 1]), __fmul_rn(s.y, swv), a[1]);
+            a[2] = __fmaf_rn(__uint_as_float(v[4 * q + 2]), __fmul_rn(s.z, swv), a[2]);
+            a[3] = __fmaf_rn(__uint_as_float(v[4 * q + 3]), __fmul_rn(s.w, swv), a[3]);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&tempty[b]);
+        if ((i & 3) == 3) mbar_arrive(&sempty[(i >> 2) & 3]);
+      }
+    }
+    // every K block has been read, so the operand ring is free: partial sums [r][token][row]
+    named_barrier(1, 128);
+    float* part = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int m = 0; m < TM; ++m) part[(r * TM + m) * 128 + threadIdx.x] = acc[r][m];
+  }
+  __syncwarp();
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+
+  // ------------------------------------------------------------ sums over the cluster and output
+  const int per = (TM + p.splits - 1) / p.splits;
+  const int n = nt * 128 + 4 * lane;  // this lane's four columns (SwiGLU: of h)
+  for (int m = rank * per + warp; m < min(rank * per + per, TM); m += kF8sThreads / 32) {
+    const int row = mt * TM + m;
+    if (row >= p.M) break;
+    float4 v[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const uint32_t at = smem_u32(ring) + ((r * TM + m) * 128 + 4 * lane) * 4;
+      v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int c = 0; c < p.splits; ++c) {
+        uint32_t from;
+        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(c));
+        const float4 t = ld_shared_cluster_f32x4(from);
+        v[r] = make_float4(__fadd_rn(v[r].x, t.x), __fadd_rn(v[r].y, t.y), __fadd_rn(v[r].z, t.z),
+                           __fadd_rn(v[r].w, t.w));
+      }
+      if (p.bias != nullptr && n < p.N) {
+        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + r * p.up_row + n));
+        v[r].x = __fadd_rn(v[r].x, __uint_as_float(b.x << 16));
+        v[r].y = __fadd_rn(v[r].y, __uint_as_float(b.x & 0xFFFF0000u));
+        v[r].z = __fadd_rn(v[r].z, __uint_as_float(b.y << 16));
+        v[r].w = __fadd_rn(v[r].w, __uint_as_float(b.y & 0xFFFF0000u));
+      }
+    }
+    float4 h = v[0];
+    if constexpr (R == 2) {
+      h.x = __fmul_rn(silu_approx(h.x), v[R - 1].x);
+      h.y = __fmul_rn(silu_approx(h.y), v[R - 1].y);
+      h.z = __fmul_rn(silu_approx(h.z), v[R - 1].z);
+      h.w = __fmul_rn(silu_approx(h.w), v[R - 1].w);
+    }
+    if constexpr (EPI == kF8SwiGLUQuant) {  // the warp holds one whole scale block
+      float a = max_nan(max_nan(fabsf(h.x), fabsf(h.y)), max_nan(fabsf(h.z), fabsf(h.w)));
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+      float inv;
+      const float s = fp8_scale(a, inv);
+      *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + int64_t(row) * p.N + n) =
+          f32x4_to_e4m3x4(__fmul_rn(h.x, inv), __fmul_rn(h.y, inv), __fmul_rn(h.z, inv), __fmul_rn(h.w, inv));
+      if (lane == 0) p.sh[int64_t(nt) * p.M + row] = s;
+    } else if (n < p.N) {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + int64_t(row) * p.N + n) =
+          make_uint2(pack_bf16x2(h.x, h.y), pack_bf16x2(h.z, h.w));
+    }
+  }
+  cluster_sync();  // the peers have read this CTA's sums
+  if (warp == 5) tmem_dealloc(tmem, Cfg::kTmem);
+}
+
 }  // namespace h3q

@@ -84,14 +84,14 @@ EncodeTiledFn encode_fn() {
   return fn;
 }
 
-// [rows, cols] int8 row-major, boxes of 128 columns x 128 rows, 128-byte swizzle;
+// [rows, cols] int8 row-major, boxes of 128 columns x box_rows rows, 128-byte swizzle;
 // reads past the edges return zeros.
-bool make_tmap_i8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols) {
+bool make_tmap_i8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int box_rows = 128) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(cols)};
-  const cuuint32_t box[2] = {128, 128};
+  const cuuint32_t box[2] = {128, static_cast<cuuint32_t>(box_rows)};
   const cuuint32_t estr[2] = {1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -202,8 +202,58 @@ bool make_tmap_f8_out(CUtensorMap* map, void* base, int64_t rows, int64_t cols, 
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+template <int EPI, int TM>
+h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w,
+                                 const float* sw, int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
+                                 int sms, cudaStream_t stream) {
+  constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
+  using Cfg = h3q::Fp8Small<R, TM>;
+  CUtensorMap tw, tx;
+  if (!make_tmap_i8(&tw, w, w_rows, K) || !make_tmap_i8(&tx, x, M, K, TM)) return H3Q_ERR_CUDA;
+  const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_small_kernel<EPI, TM>);
+  if (ensure_smem_attr(kernel, 232448) != cudaSuccess) return H3Q_ERR_CUDA;
+  h3q::Fp8SmallParams p{};
+  p.M = static_cast<int>(M);
+  p.N = static_cast<int>(N_out);
+  p.KB = static_cast<int>((K + 127) / 128);
+  p.num_m = static_cast<int>((M + TM - 1) / TM);
+  p.num_n = static_cast<int>((N_out + 127) / 128);
+  p.up_row = R == 2 ? static_cast<int>(N_out) : 0;
+  p.swiglu_rows = p.up_row / 128;
+  p.sx = sx;
+  p.sw = sw;
+  p.bias = static_cast<const __nv_bfloat16*>(bias);
+  p.out = out;
+  p.sh = sh;
+  p.wait_limit_ns = g_wait_limit_ns.load();
+  // Split the K axis while another CTA an SM fits and each keeps at least four K blocks.
+  const int64_t tiles = int64_t(p.num_m) * p.num_n;
+  const int resident = R * TM <= 64 ? 2 : 1;  // CTAs an SM (registers)
+  int splits = 1;
+  while (splits < 8 && tiles * splits * 2 <= int64_t(sms) * resident && p.KB >= splits * 2 * 4) splits *= 2;
+  p.splits = splits;
+  const bool two = tiles * splits > sms && resident == 2;
+  const int room = (two ? 113 * 1024 : 226 * 1024) - Cfg::kFixed;
+  p.stages = std::min(std::min(room / Cfg::kStage, h3q::kF8sMaxStages), std::max(2, (p.KB + splits - 1) / splits));
+  const size_t ring = std::max<size_t>(size_t(p.stages) * Cfg::kStage, Cfg::kPartials);
+  const size_t smem = ring + Cfg::kFixed;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
+  cfg.blockDim = dim3(h3q::kF8sThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = static_cast<unsigned>(splits);
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, h3q::gemm_fp8_small_kernel<EPI, TM>, tw, tx, p) == cudaSuccess ? H3Q_OK
+                                                                                              : H3Q_ERR_CUDA;
+}
+
 template <int EPI>
-h3q_status launch_gemm_fp8(const uint8_t* a, const float* sx, int64_t M, int64_t K, const uint8_t* b, const float* sw,
+h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, int64_t K, const uint8_t* b, const float* sw,
                            int64_t b_rows, int64_t N_out, const void* bias, void* out, float* sh,
                            cudaStream_t stream) {
   CUtensorMap ta, tb, tout;
@@ -249,12 +299,27 @@ h3q_status launch_gemm_fp8(const uint8_t* a, const float* sx, int64_t M, int64_t
 // token are split over several warps.
 constexpr int kQkWarpsPerSm = 16;
 
+// At most this many tokens: the kernel for few tokens.
+constexpr int64_t kF8SmallTokens = 128;
+
+template <int EPI>
+h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w, const float* sw,
+                           int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
+                           cudaStream_t stream) {
+  const int sms = sm_count();
+  if (sms <= 0) return H3Q_ERR_CUDA;
+  if (M > kF8SmallTokens) return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
+  if (M <= 16) return launch_gemm_fp8_small<EPI, 16>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
+  if (M <= 32) return launch_gemm_fp8_small<EPI, 32>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
+  return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
+}
+
 template <int G>
 void launch_qk(const h3q::QkParams& p, bool interleaved, int sms, cudaStream_t stream) {
   const int64_t steps = (p.Hq + 32 / G - 1) / (32 / G) + (p.Hk + 32 / G - 1) / (32 / G);
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(steps, 65535), int64_t(sms) * kQkWarpsPerSm / p.S));
   const unsigned warps = static_cast<unsigned>(std::min<int64_t>(8, p.S));
-  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((p.S + warps - 1) / warps, int64_t(sms) * 8)),
+  const dim3 grid(static_cast<unsigned>(std::min<int64_t>((p.S + warps - 1) / warps, int64_t(sms) * 2)),
                   static_cast<unsigned>(parts));
   if (interleaved)
     h3q::qk_norm_rope_kernel<G, true><<<grid, 32 * warps, 0, stream>>>(p);

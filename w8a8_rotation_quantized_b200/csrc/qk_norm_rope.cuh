@@ -9,9 +9,10 @@
 // one token at a time, so its lanes load the token's table row once for all of its
 // heads and fold the norm's weights into it: with C_i = w_i c_i and S_i = -+w_p s_i (p
 // the partner of i), the result is r (x_i C_i + x_p S_i), three operations an element.
-// Four heads a lane group are in flight at once. The kernel reads and writes every
-// element once and is bound by memory: 84 heads of 128 over 16384 tokens take 704 MB.
-// Few tokens are spread over more warps by splitting the heads.
+// Eight heads a lane group are in flight at once (two blocks an SM: 129 us at 84 heads
+// of 128 over 16384 tokens; four in flight 149, four at three or four blocks 135-143).
+// The kernel reads and writes every element once and is bound by memory: 704 MB there,
+// 83% of the copy rate. Few tokens are spread over more warps by splitting the heads.
 //
 // Each lane holds its elements until they are stored, and a group's loads come
 // before its stores, so q_out and k_out may be q and k themselves.
@@ -48,9 +49,9 @@ __device__ __forceinline__ void qk_load8(const __nv_bfloat16* p, float (&v)[8]) 
 // G: lanes per head (a power of two, 8 G >= D). Grid: x tokens (warps stride over
 // them), y the part of the heads.
 template <int G, bool INTER>
-__global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
+__global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) {
   constexpr int kHeads = 32 / G;  // heads a warp step takes
-  constexpr int kUnroll = 4;      // steps in flight
+  constexpr int kUnroll = 8;      // steps in flight
   const int lane = threadIdx.x & 31;
   const int l = lane % G, sub = lane / G;
   const bool live = 8 * l < p.D;
@@ -104,17 +105,20 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
       const __nv_bfloat16* wt = which ? p.wk : p.wq;
       const __nv_bfloat16* src = (which ? p.k + t * p.ldk : p.q + t * p.ldq) + 8 * l;
       __nv_bfloat16* dst = (which ? p.ko + t * p.ldko : p.qo + t * p.ldqo) + 8 * l;
-      float cw[8], sw[8];
+      float2 cw[4], sw[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) cw[i] = c[i], sw[i] = s[i];
+      for (int i = 0; i < 4; ++i) {
+        cw[i] = make_float2(c[2 * i], c[2 * i + 1]);
+        sw[i] = make_float2(s[2 * i], s[2 * i + 1]);
+      }
       if (wt != nullptr && live) {
         float wi[8], wp[8];
         qk_load8(wt + 8 * l, wi);
         qk_load8(wt + 8 * (partner % G), wp);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          cw[i] = __fmul_rn(c[i], wi[i]);
-          sw[i] = __fmul_rn(s[i], INTER ? wp[i ^ 1] : wp[i]);
+        for (int i = 0; i < 4; ++i) {
+          cw[i] = __fmul2_rn(cw[i], make_float2(wi[2 * i], wi[2 * i + 1]));
+          sw[i] = __fmul2_rn(sw[i], INTER ? make_float2(wp[2 * i + 1], wp[2 * i]) : make_float2(wp[2 * i], wp[2 * i + 1]));
         }
       }
       for (int st = lo; st < hi; st += kUnroll) {
@@ -130,31 +134,29 @@ __global__ void __launch_bounds__(256) qk_norm_rope_kernel(const QkParams p) {
           if (st + u >= hi) break;  // the same for the whole warp
           const int h = (st + u) * kHeads + sub;
           const uint32_t w[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
-          float x[8], y[8];
-          float ss = 0.0f;
+          float2 x[4], y[4];
+          float2 s2 = make_float2(0.0f, 0.0f);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[2 * i] = __uint_as_float(w[i] << 16);
-            x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-            ss = __fmaf_rn(x[2 * i], x[2 * i], ss);
-            ss = __fmaf_rn(x[2 * i + 1], x[2 * i + 1], ss);
+            x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+            s2 = __ffma2_rn(x[i], x[i], s2);
           }
+          float ss = s2.x + s2.y;
 #pragma unroll
           for (int o = 1; o < G; o <<= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
           const float r = rsqrtf(__fmaf_rn(ss, inv_d, p.eps));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const uint32_t o = INTER ? w[i] : __shfl_sync(0xFFFFFFFFu, w[i], partner);
-            const float p0 = __uint_as_float(INTER ? o & 0xFFFF0000u : o << 16);
-            const float p1 = __uint_as_float(INTER ? o << 16 : o & 0xFFFF0000u);
-            y[2 * i] = __fmul_rn(__fmaf_rn(x[2 * i], cw[2 * i], __fmul_rn(p0, sw[2 * i])), r);
-            y[2 * i + 1] = __fmul_rn(__fmaf_rn(x[2 * i + 1], cw[2 * i + 1], __fmul_rn(p1, sw[2 * i + 1])), r);
+            const float2 xp = INTER ? make_float2(x[i].y, x[i].x)
+                                    : make_float2(__uint_as_float(o << 16), __uint_as_float(o & 0xFFFF0000u));
+            y[i] = __fmul2_rn(__ffma2_rn(x[i], cw[i], __fmul2_rn(xp, sw[i])), make_float2(r, r));
           }
           if (live && h < H) {
             uint32_t out[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+              const __nv_bfloat162 b = __floats2bfloat162_rn(y[i].x, y[i].y);
               out[i] = *reinterpret_cast<const uint32_t*>(&b);
             }
             *reinterpret_cast<uint4*>(dst + int64_t(h) * p.D) = make_uint4(out[0], out[1], out[2], out[3]);
