@@ -322,54 +322,89 @@ def h3q_attention_prep(q, k, v, H, qq, qs, kq, ks, vt, stream=None) -> None:
                                   _ptr(vt), _stream(stream)), "h3q_attention_prep")
 
 
-def _on_device(name, fn, device, stream, *args):
-    """Calls fn(*args, stream) with `device` current, on `stream` or the device's current stream."""
-    import torch
+# The fp8 and query/key calls are also made for single tokens, where the checks of their
+# operands would cost more than the kernel: they test each operand in one expression and
+# come to the checks above only to name the fault.
+_torch = None
+
+
+def _t():
+    """torch, imported on first use."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _is(t, dtype, shape, index):
+    """t is a dense tensor of this dtype and shape on CUDA device `index`."""
+    return (t is not None and t.dtype is dtype and t.is_cuda and t.get_device() == index and t.shape == shape
+            and t.is_contiguous())
+
+
+def _run(name, fn, index, stream, *args):
+    """Calls fn(*args, stream) with CUDA device `index` current, on `stream` or that device's
+    current stream."""
+    torch = _t()
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        stream = torch.cuda.current_stream(index)
     stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, stream), name)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, stream)
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, stream), name)
+        with torch.cuda.device(index):
+            status = fn(*args, stream)
+    if status != H3Q_OK:
+        raise H3QError(status, name)
 
 
-def _fp8_x_dtype(w, x):
-    """The dtype code of an fp8 quantizer's input [rows, K]."""
-    import torch
-    if x is not None and x.dtype == torch.bfloat16:
-        _need(w, "x", x, "bf16", (None, None))
-        return H3Q_DTYPE_BF16
-    _need(w, "x", x, "f32", (None, None))
-    return H3Q_DTYPE_F32
+def _fp8_quantizer(w, fn, x, codes, scales, weight, stream):
+    torch = _t()
+    if x is not None and x.dim() == 2 and x.is_cuda:
+        rows, K = x.shape
+        index = x.get_device()
+        KB = (K + 127) // 128
+        dt = H3Q_DTYPE_BF16 if x.dtype is torch.bfloat16 else H3Q_DTYPE_F32
+        want = ((rows + 127) // 128, KB) if weight else (KB, rows)
+        if (_is(x, torch.bfloat16 if dt == H3Q_DTYPE_BF16 else torch.float32, (rows, K), index)
+                and _is(codes, torch.float8_e4m3fn, (rows, K), index) and _is(scales, torch.float32, want, index)):
+            return _run(w, fn, index, stream, x.data_ptr(), dt, rows, K, codes.data_ptr(), scales.data_ptr())
+    rows, K = _need(w, "w" if weight else "x", x, "bf16" if x is not None and x.dtype == torch.bfloat16 else "f32",
+                    (None, None)).shape
+    KB = (K + 127) // 128
+    _need(w, "wq" if weight else "xq", codes, "e4m3", (rows, K), x.device)
+    _need(w, "sw" if weight else "sx", scales, "f32", ((rows + 127) // 128, KB) if weight else (KB, rows), x.device)
 
 
 def h3q_fp8_quantize(x, xq, sx, stream=None) -> None:
     """x [M, K] bf16 or fp32 -> xq float8_e4m3fn [M, K], sx fp32 [ceil(K/128), M]: one scale
     per token and 128 elements."""
-    w = "h3q_fp8_quantize"
-    dt = _fp8_x_dtype(w, x)
-    M, K = x.shape
-    dev = x.device
-    _need(w, "xq", xq, "e4m3", (M, K), dev)
-    _need(w, "sx", sx, "f32", ((K + 127) // 128, M), dev)
-    _on_device(w, lib.h3q_fp8_quantize, dev, stream, x.data_ptr(), dt, M, K, xq.data_ptr(), sx.data_ptr())
+    _fp8_quantizer("h3q_fp8_quantize", lib.h3q_fp8_quantize, x, xq, sx, False, stream)
 
 
 def h3q_fp8_prepare_weight(w, wq, sw, stream=None) -> None:
     """w [N, K] bf16 or fp32 -> wq float8_e4m3fn [N, K], sw fp32 [ceil(N/128), ceil(K/128)]:
     one scale per 128 x 128 block."""
-    wh = "h3q_fp8_prepare_weight"
-    dt = _fp8_x_dtype(wh, w)
-    N, K = w.shape
-    dev = w.device
-    _need(wh, "wq", wq, "e4m3", (N, K), dev)
-    _need(wh, "sw", sw, "f32", ((N + 127) // 128, (K + 127) // 128), dev)
-    _on_device(wh, lib.h3q_fp8_prepare_weight, dev, stream, w.data_ptr(), dt, N, K, wq.data_ptr(), sw.data_ptr())
+    _fp8_quantizer("h3q_fp8_prepare_weight", lib.h3q_fp8_prepare_weight, w, wq, sw, True, stream)
 
 
-def _fp8_operands(w, xq, sx, wq, sw, bias):
+def _fp8_operands(w, xq, sx, wq, sw, bias, out, out_dtype, halved, sh=None):
+    """M, K, N and the device's index of an fp8 product's operands; raises ValueError."""
+    torch = _t()
+    if xq is not None and wq is not None and xq.dim() == 2 and wq.dim() == 2 and xq.is_cuda:
+        M, K = xq.shape
+        N = wq.shape[0]
+        index = xq.get_device()
+        KB = (K + 127) // 128
+        e4m3, f32 = torch.float8_e4m3fn, torch.float32
+        out_shape = (M, N // 2 if halved else N)
+        if (_is(xq, e4m3, (M, K), index) and _is(wq, e4m3, (N, K), index) and _is(sx, f32, (KB, M), index)
+                and _is(sw, f32, ((N + 127) // 128, KB), index)
+                and (bias is None or _is(bias, torch.bfloat16, (N,), index))
+                and _is(out, torch.bfloat16 if out_dtype == "bf16" else e4m3, out_shape, index)
+                and (out_dtype == "bf16" or _is(sh, f32, (N // 256, M), index))):
+            return M, K, N, index
     M, K = _need(w, "xq", xq, "e4m3", (None, None)).shape
     dev = xq.device
     N = _need(w, "wq", wq, "e4m3", (None, K), dev).shape[0]
@@ -378,29 +413,29 @@ def _fp8_operands(w, xq, sx, wq, sw, bias):
     _need(w, "sw", sw, "f32", ((N + 127) // 128, KB), dev)
     if bias is not None:
         _need(w, "bias", bias, "bf16", (N,), dev)
-    return M, K, N, dev
+    _need(w, "y" if out_dtype == "bf16" else "hq", out, out_dtype, (M, N // 2 if halved else N), dev)
+    if out_dtype != "bf16":
+        _need(w, "sh", sh, "f32", (N // 256, M), dev)
+    return M, K, N, dev.index
 
 
 def h3q_linear_fp8(xq, sx, wq, sw, y, bias=None, epilogue=H3Q_EPI_NONE, stream=None) -> None:
     """y bf16 [M, N] = block-scaled fp8 product of xq (sx) and wq (sw), + bias; SwiGLU
     epilogue: y [M, N/2]."""
     w = "h3q_linear_fp8"
-    M, K, N, dev = _fp8_operands(w, xq, sx, wq, sw, bias)
     epilogue = int(epilogue)
-    _need(w, "y", y, "bf16", (M, N // 2 if epilogue == H3Q_EPI_SWIGLU else N), dev)
-    _on_device(w, lib.h3q_linear_fp8, dev, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(), sw.data_ptr(), N,
-               _ptr(bias), epilogue, y.data_ptr())
+    M, K, N, index = _fp8_operands(w, xq, sx, wq, sw, bias, y, "bf16", epilogue == H3Q_EPI_SWIGLU)
+    _run(w, lib.h3q_linear_fp8, index, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(), sw.data_ptr(), N,
+         _ptr(bias), epilogue, y.data_ptr())
 
 
 def h3q_linear_fp8_swiglu_quant(xq, sx, wq, sw, hq, sh, bias=None, stream=None) -> None:
     """hq float8_e4m3fn [M, F], sh fp32 [F/128, M] = quantized SwiGLU of the gate/up product
     (wq [2F, K], gate rows first): the operands of the down projection."""
     w = "h3q_linear_fp8_swiglu_quant"
-    M, K, N, dev = _fp8_operands(w, xq, sx, wq, sw, bias)
-    _need(w, "hq", hq, "e4m3", (M, N // 2), dev)
-    _need(w, "sh", sh, "f32", (N // 256, M), dev)
-    _on_device(w, lib.h3q_linear_fp8_swiglu_quant, dev, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(),
-               sw.data_ptr(), N, _ptr(bias), hq.data_ptr(), sh.data_ptr())
+    M, K, N, index = _fp8_operands(w, xq, sx, wq, sw, bias, hq, "e4m3", True, sh)
+    _run(w, lib.h3q_linear_fp8_swiglu_quant, index, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(),
+         sw.data_ptr(), N, _ptr(bias), hq.data_ptr(), sh.data_ptr())
 
 
 H3Q_QK_MAX_D = 256
@@ -412,31 +447,37 @@ def h3q_qk_norm_rope(q, k, Hq, Hk, D, cos, sin, q_out, k_out, q_weight=None, k_w
     Hk = 0), then the rotation by row positions[t] (int32 [S]; None: row t) of cos, sin
     (fp32 [P, rot/2]; None: no rotation). q_out, k_out: the same shapes, may be q and k."""
     w = "h3q_qk_norm_rope"
-    S = _need(w, "q", q, "bf16", (None, None), dense=False).shape[0]
-    dev = q.device
-    views = [("q", q, Hq), ("q_out", q_out, Hq)]
-    if Hk:
-        views += [("k", k, Hk), ("k_out", k_out, Hk)]
-    for name, t, h in views:
-        _need(w, name, t, "bf16", (S, None), dev, dense=False)
-        if t.shape[1] < h * D:
-            raise ValueError(f"{w}: {name} must have at least {h * D} columns, got {t.shape[1]}")
+    bf16, f32 = _t().bfloat16, _t().float32
+    if q is None or q.dim() != 2 or not q.is_cuda:
+        _need(w, "q", q, "bf16", (None, None), dense=False)
+    S, index = q.shape[0], q.get_device()
+    lds = []
+    for name, t, heads in (("q", q, Hq), ("q_out", q_out, Hq), ("k", k, Hk), ("k_out", k_out, Hk)):
+        if heads == 0 and name[0] == "k":
+            lds.append(0)
+            continue
+        width = heads * D
+        if (t is None or t.dtype is not bf16 or t.dim() != 2 or t.get_device() != index or t.shape[0] != S
+                or t.shape[1] < width or (t.stride(1) != 1 and t.shape[1] > 1)):
+            _need(w, name, t, "bf16", (S, None), q.device, dense=False)
+            raise ValueError(f"{w}: {name} must have at least {width} columns, got {t.shape[1]}")
+        lds.append(t.stride(0) if S > 1 else width)  # the stride of a single row means nothing
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None:
-            _need(w, name, t, "bf16", (D,), dev)
+        if t is not None and not _is(t, bf16, (D,), index):
+            _need(w, name, t, "bf16", (D,), q.device)
     P = half = 0
     if cos is not None:
-        P, half = _need(w, "cos", cos, "f32", (None, None), dev).shape
-        _need(w, "sin", sin, "f32", (P, half), dev)
+        if not (cos.dim() == 2 and _is(cos, f32, cos.shape, index) and _is(sin, f32, cos.shape, index)):
+            P, half = _need(w, "cos", cos, "f32", (None, None), q.device).shape
+            _need(w, "sin", sin, "f32", (P, half), q.device)
+        P, half = cos.shape
     elif sin is not None:
         raise ValueError(f"{w}: sin without cos")
-    if positions is not None:
-        _need(w, "positions", positions, "i32", (S,), dev)
-    # the stride of a single row means nothing (torch leaves any value there)
-    ldq, ldqo, ldk, ldko = [_ld(t) if S > 1 else h * D for _, t, h in views] + ([] if Hk else [0, 0])
-    _on_device(w, lib.h3q_qk_norm_rope, dev, stream, q.data_ptr(), _ptr(k) if Hk else None, S, Hq, Hk, D, ldq, ldk,
-               _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos), _ptr(sin), P, 2 * half, int(bool(interleaved)),
-               _ptr(positions), q_out.data_ptr(), _ptr(k_out) if Hk else None, ldqo, ldko)
+    if positions is not None and not _is(positions, _t().int32, (S,), index):
+        _need(w, "positions", positions, "i32", (S,), q.device)
+    _run(w, lib.h3q_qk_norm_rope, index, stream, q.data_ptr(), k.data_ptr() if Hk else None, S, Hq, Hk, D, lds[0],
+         lds[2], _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos), _ptr(sin), P, 2 * half, int(bool(interleaved)),
+         _ptr(positions), q_out.data_ptr(), k_out.data_ptr() if Hk else None, lds[1], lds[3])
 
 
 def h3q_gemm_s32(xq, wq, acc, stream=None) -> None:

@@ -156,6 +156,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = kb * 128 + 8 * lane;
   const int64_t m0 = int64_t(rb) * kF8QuantRows;
+  grid_dependency_wait();
   Fp8Chunk<T> v[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -382,6 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  grid_dependency_wait();
 
   auto tile_at = [&](int tile, int& mb, int& nb) {
     const int per_group = p.group_m * p.num_n;
@@ -643,17 +645,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 // columns a lane), so the result does not depend on timing and nothing is kept in
 // global memory.
 constexpr int kF8sMaxStages = 12;
-constexpr int kF8sThreads = 256;  // four promotion warps, operands, MMA, scales, one idle until the output
+constexpr int kF8sThreads = 384;  // eight promotion warps, operands, MMA, scales, one idle until the output
 constexpr int kF8sScaleRing = 16;
 
 template <int R, int TM>
 struct Fp8Small {
   static constexpr int kStage = R * 128 * 128 + TM * 128;
   static constexpr int kCols = R * TM;                       // tensor-memory columns of one K block
+  static constexpr int kHalf = kCols / 2;                    // columns of a promotion thread
   static constexpr int kBufs = kCols >= 256 ? 2 : 4;
   static constexpr int kTmem = kCols * kBufs < 32 ? 32 : kCols * kBufs;
   static constexpr int kPartials = R * TM * 128 * 4;
-  static_assert(kPartials <= 2 * kStage, "the partial sums fit in the operand ring");
+  static_assert(kPartials <= 3 * kStage, "the partial sums fit in the operand ring");
   static constexpr int kScaleSlot = TM * 4 + 16;
   static constexpr int kFixed = kF8sScaleRing * kScaleSlot + 512 /*barriers*/ + 1024 /*align*/;
 };
@@ -682,7 +685,15 @@ __device__ __forceinline__ void mma_fp8(uint32_t d_tmem, uint64_t a_desc, uint64
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+// 8, 16 or 32 consecutive columns of the warp's lanes, and the wait that the loaded
+// registers depend on.
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
       "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
@@ -691,12 +702,21 @@ __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
       : "r"(taddr));
 }
 
-__device__ __forceinline__ void tmem_ld_wait16(uint32_t (&r)[16]) {
+__device__ __forceinline__ void tmem_ld_cols(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+
+__device__ __forceinline__ void tmem_ld_cols_wait(uint32_t (&r)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
+
+__device__ __forceinline__ void tmem_ld_cols_wait(uint32_t (&r)[16]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
                  "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]),
                  "+r"(r[15])::"memory");
 }
+
+__device__ __forceinline__ void tmem_ld_cols_wait(uint32_t (&r)[32]) { tmem_ld_wait32(r); }
 
 __device__ __forceinline__ float4 ld_shared_cluster_f32x4(uint32_t cluster_addr) {
   float4 v;
@@ -742,26 +762,41 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
   const int nkb = static_cast<int>(int64_t(p.KB) * (rank + 1) / p.splits) - kb0;
   const uint64_t limit = p.wait_limit_ns;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < S; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+  // The operand warp sets up the barriers and sends for the first stages at once, while
+  // tensor memory is allocated.
+  const bool one = elect_one();
+  auto load_stage = [&](int stage, int i) {
+    uint8_t* dst = ring + stage * Cfg::kStage;
+    const uint64_t pol = policy_evict_normal();
+    const int k = (kb0 + i) * 128;
+    mbar_arrive_expect_tx(&full[stage], Cfg::kStage);
+    tma_load_2d(dst, &tmW, &full[stage], k, nt * 128, pol);
+    if (R == 2) tma_load_2d(dst + 128 * 128, &tmW, &full[stage], k, p.up_row + nt * 128, pol);
+    tma_load_2d(dst + R * 128 * 128, &tmX, &full[stage], k, mt * TM, pol);
+  };
+  if (warp == 8) {
+    if (one) {
+      tma_prefetch_desc(&tmW);
+      tma_prefetch_desc(&tmX);
+      for (int s = 0; s < S; ++s) {
+        mbar_init(&full[s], 1);
+        mbar_init(&empty[s], 1);
+      }
+      for (int b = 0; b < 4; ++b) {
+        mbar_init(&tfull[b], 1);
+        mbar_init(&tempty[b], 8);
+        mbar_init(&sfull[b], 32);
+        mbar_init(&sempty[b], 8);
+      }
+      mbar_init(drain, 1);
+      *abort_flag = 0;
+      fence_mbarrier_init();
     }
-    for (int b = 0; b < 4; ++b) {
-      mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 4);
-      mbar_init(&sfull[b], 32);
-      mbar_init(&sempty[b], 4);
-    }
-    mbar_init(drain, 1);
-    *abort_flag = 0;
-    fence_mbarrier_init();
+    grid_dependency_wait();
+    if (one)
+      for (int s = 0; s < min(S, nkb); ++s) load_stage(s, s);
   }
-  if (warp == 4 && lane == 0) {
-    tma_prefetch_desc(&tmW);
-    tma_prefetch_desc(&tmX);
-  }
-  if (warp == 5) {
+  if (warp == 9) {
     tmem_alloc(tmem_slot, Cfg::kTmem);
     tmem_relinquish();
   }
@@ -769,23 +804,15 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  grid_dependency_wait();
 
-  if (warp == 4) {
+  if (warp == 8) {
     // ------------------------------------------------------------ operand tiles
-    const bool one = elect_one();
-    const uint64_t pol = policy_evict_normal();
-    int stage = 0, i = 0;
+    int stage = 0, i = min(S, nkb);  // the first round is on its way
     uint32_t phase = 0;
     for (; i < nkb; ++i) {
-      if (!mbar_wait_bounded_warp(&empty[stage], phase ^ 1u, limit, abort_flag)) break;
-      if (one) {
-        uint8_t* dst = ring + stage * Cfg::kStage;
-        const int k = (kb0 + i) * 128;
-        mbar_arrive_expect_tx(&full[stage], Cfg::kStage);
-        tma_load_2d(dst, &tmW, &full[stage], k, nt * 128, pol);
-        if (R == 2) tma_load_2d(dst + 128 * 128, &tmW, &full[stage], k, p.up_row + nt * 128, pol);
-        tma_load_2d(dst + R * 128 * 128, &tmX, &full[stage], k, mt * TM, pol);
-      }
+      if (!mbar_wait_bounded_warp(&empty[stage], phase, limit, abort_flag)) break;
+      if (one) load_stage(stage, i);
       if (++stage == S) {
         stage = 0;
         phase ^= 1u;
@@ -795,10 +822,9 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
     if (i < nkb)
       for (int m = i - 1; m >= 0 && m >= i - S; --m)
         mbar_wait_bounded(&full[m % S], static_cast<uint32_t>((m / S) & 1), limit, nullptr);
-  } else if (warp == 5) {
+  } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc = idesc_fp8(128, TM);
-    const bool one = elect_one();
     int stage = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nkb; ++i) {
@@ -827,7 +853,7 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
     }
     if (one) mma_commit(drain);
     mbar_wait_bounded(drain, 0, limit, nullptr);
-  } else if (warp == 6) {
+  } else if (warp == 10) {
     // ------------------------------------------------------------ scales, handed over by fours
     bool ok = true;
     for (int i = 0; ok && i < nkb; ++i) {
@@ -848,54 +874,60 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
     }
     cp_async_commit();
     cp_async_wait<0>();
-  } else if (warp < 4) {
+  } else if (warp < 8) {
     // ------------------------------------------------------------ promotion: thread = weight row
-    float acc[R][TM];
+    // Warps 0..7: TMEM lanes 32*(w%4) .. +31 and one half of the columns: with SwiGLU
+    // gate or up, else half of the tokens.
+    const int half = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    constexpr int kChunk = Cfg::kHalf < 32 ? Cfg::kHalf : 32;
+    float2 acc[Cfg::kHalf / 2];
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int m = 0; m < TM; ++m) acc[r][m] = 0.0f;
-    const uint32_t tlane = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+    for (int m = 0; m < Cfg::kHalf / 2; ++m) acc[m] = make_float2(0.0f, 0.0f);
+    const uint32_t tcol = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + static_cast<uint32_t>(half * Cfg::kHalf);
+    const uint32_t sx_at = R == 2 ? 0 : half * Cfg::kHalf * 4, sw_at = TM * 4 + (R == 2 ? half * 4 : 0);
 #pragma unroll 1
     for (int i = 0; i < nkb; ++i) {
       const int b = i % Cfg::kBufs;
       if ((i & 3) == 0 && !mbar_wait_bounded_lazy(&sfull[(i >> 2) & 3], (i >> 4) & 1, limit, abort_flag)) break;
+      const uint32_t slot = smem_u32(scale_ring) + (i & (kF8sScaleRing - 1)) * Cfg::kScaleSlot;
+      const float swv = ld_shared_f32(slot + sw_at);
       if (!mbar_wait_bounded_lazy(&tfull[b], (i / Cfg::kBufs) & 1, limit, abort_flag)) break;
       tc_fence_after();
-      const uint32_t slot = smem_u32(scale_ring) + (i & (kF8sScaleRing - 1)) * Cfg::kScaleSlot;
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
-        const float swv = ld_shared_f32(slot + TM * 4 + r * 4);
+      for (int c = 0; c < Cfg::kHalf / kChunk; ++c) {
+        uint32_t v[kChunk];
+        tmem_ld_cols(tcol + static_cast<uint32_t>(b * Cfg::kCols + c * kChunk), v);
+        tmem_ld_cols_wait(v);
+        if (c == Cfg::kHalf / kChunk - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[b]);
+        }
 #pragma unroll
-        for (int c = 0; c < TM / 16; ++c) {
-          uint32_t v[16];
-          tmem_ld16(tlane + static_cast<uint32_t>(b * Cfg::kCols + r * TM + 16 * c), v);
-          tmem_ld_wait16(v);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float4 s = ld_shared_f32x4(slot + (16 * c + 4 * q) * 4);
-            float* a = &acc[r][16 * c + 4 * q];
-            a[0] = __fmaf_rn(__uint_as_float(v[4 * q]), __fmul_rn(s.x, swv), a[0]);
-            a[1] = __fmaf_rn(__uint_as_float(v[4 * q + 1]), __fmul_rn(s.y, swv), a[1]);
-            a[2] = __fmaf_rn(__uint_as_float(v[4 * q + 2]), __fmul_rn(s.z, swv), a[2]);
-            a[3] = __fmaf_rn(__uint_as_float(v[4 * q + 3]), __fmul_rn(s.w, swv), a[3]);
-          }
+        for (int q = 0; q < kChunk / 4; ++q) {
+          const float4 s = ld_shared_f32x4(slot + sx_at + (c * kChunk + 4 * q) * 4);
+          float2* a = &acc[(c * kChunk + 4 * q) / 2];
+          const float2 w2 = make_float2(swv, swv);
+          a[0] = __ffma2_rn(make_float2(__uint_as_float(v[4 * q]), __uint_as_float(v[4 * q + 1])),
+                            __fmul2_rn(make_float2(s.x, s.y), w2), a[0]);
+          a[1] = __ffma2_rn(make_float2(__uint_as_float(v[4 * q + 2]), __uint_as_float(v[4 * q + 3])),
+                            __fmul2_rn(make_float2(s.z, s.w), w2), a[1]);
         }
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&tempty[b]);
-        if ((i & 3) == 3) mbar_arrive(&sempty[(i >> 2) & 3]);
+      if ((i & 3) == 3) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[(i >> 2) & 3]);
       }
     }
-    // every K block has been read, so the operand ring is free: partial sums [r][token][row]
-    named_barrier(1, 128);
+    // every K block has been read, so the operand ring is free: partial sums [column][row]
+    named_barrier(1, 256);
     float* part = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int r = 0; r < R; ++r)
-#pragma unroll
-      for (int m = 0; m < TM; ++m) part[(r * TM + m) * 128 + threadIdx.x] = acc[r][m];
+    for (int m = 0; m < Cfg::kHalf / 2; ++m) {
+      part[(half * Cfg::kHalf + 2 * m) * 128 + row] = acc[m].x;
+      part[(half * Cfg::kHalf + 2 * m + 1) * 128 + row] = acc[m].y;
+    }
   }
   __syncwarp();
   tc_fence_before();
@@ -914,9 +946,14 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
       const uint32_t at = smem_u32(ring) + ((r * TM + m) * 128 + 4 * lane) * 4;
       v[r] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
       for (int c = 0; c < p.splits; ++c) {
-        uint32_t from;
-        asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(c));
-        const float4 t = ld_shared_cluster_f32x4(from);
+        float4 t;
+        if (p.splits == 1) {
+          t = ld_shared_f32x4(at);
+        } else {
+          uint32_t from;
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(from) : "r"(at), "r"(c));
+          t = ld_shared_cluster_f32x4(from);
+        }
         v[r] = make_float4(__fadd_rn(v[r].x, t.x), __fadd_rn(v[r].y, t.y), __fadd_rn(v[r].z, t.z),
                            __fadd_rn(v[r].w, t.w));
       }
@@ -949,8 +986,8 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
           make_uint2(pack_bf16x2(h.x, h.y), pack_bf16x2(h.z, h.w));
     }
   }
-  cluster_sync();  // the peers have read this CTA's sums
-  if (warp == 5) tmem_dealloc(tmem, Cfg::kTmem);
+  cluster_sync_relaxed();  // the peers have read this CTA's sums
+  if (warp == 9) tmem_dealloc(tmem, Cfg::kTmem);
 }
 
 }  // namespace h3q

@@ -99,9 +99,12 @@ bool make_tmap_i8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols
 }
 
 int sm_count() {
+  static std::atomic<int> known[64];  // a property of the device: looked up once
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64 && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
   if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev >= 0 && dev < 64) known[dev].store(n, std::memory_order_relaxed);
   return n;
 }
 
@@ -202,6 +205,27 @@ bool make_tmap_f8_out(CUtensorMap* map, void* base, int64_t rows, int64_t cols, 
              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Launches `kernel` as a programmatic dependent of what precedes it in the stream (see
+// grid_dependency_wait), with a cluster of `cluster` blocks where that is above zero.
+template <typename... Params, typename... Args>
+h3q_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threads, size_t smem, unsigned cluster,
+                            cudaStream_t stream, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 0 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+}
+
 template <int EPI, int TM>
 h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w,
                                  const float* sw, int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
@@ -234,22 +258,10 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   p.splits = splits;
   const bool two = tiles * splits > sms && resident == 2;
   const int room = (two ? 113 * 1024 : 226 * 1024) - Cfg::kFixed;
-  p.stages = std::min(std::min(room / Cfg::kStage, h3q::kF8sMaxStages), std::max(2, (p.KB + splits - 1) / splits));
-  const size_t ring = std::max<size_t>(size_t(p.stages) * Cfg::kStage, Cfg::kPartials);
-  const size_t smem = ring + Cfg::kFixed;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * splits));
-  cfg.blockDim = dim3(h3q::kF8sThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(splits);
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, h3q::gemm_fp8_small_kernel<EPI, TM>, tw, tx, p) == cudaSuccess ? H3Q_OK
-                                                                                              : H3Q_ERR_CUDA;
+  p.stages = std::min(std::min(room / Cfg::kStage, h3q::kF8sMaxStages), std::max(3, (p.KB + splits - 1) / splits));
+  const size_t smem = size_t(p.stages) * Cfg::kStage + Cfg::kFixed;
+  return launch_dependent(h3q::gemm_fp8_small_kernel<EPI, TM>, dim3(static_cast<unsigned>(tiles * splits)),
+                          h3q::kF8sThreads, smem, static_cast<unsigned>(splits), stream, tw, tx, p);
 }
 
 template <int EPI>
@@ -291,8 +303,8 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
-  h3q::gemm_fp8_kernel<EPI><<<2 * pairs, h3q::kF8Threads, h3q::kF8Smem, stream>>>(ta, tb, tout, p);
-  return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+  return launch_dependent(h3q::gemm_fp8_kernel<EPI>, dim3(2 * pairs), h3q::kF8Threads, h3q::kF8Smem, 0, stream, ta, tb,
+                          tout, p);
 }
 
 // Warps of qk_norm_rope wanted per SM: below that many tokens an SM, the heads of a
@@ -311,20 +323,19 @@ h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t
   if (M > kF8SmallTokens) return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
   if (M <= 16) return launch_gemm_fp8_small<EPI, 16>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
   if (M <= 32) return launch_gemm_fp8_small<EPI, 32>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
-  return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
+  if (M <= 64) return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
+  return launch_gemm_fp8_small<EPI, 128>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
 }
 
 template <int G>
-void launch_qk(const h3q::QkParams& p, bool interleaved, int sms, cudaStream_t stream) {
+h3q_status launch_qk(const h3q::QkParams& p, bool interleaved, int sms, cudaStream_t stream) {
   const int64_t steps = (p.Hq + 32 / G - 1) / (32 / G) + (p.Hk + 32 / G - 1) / (32 / G);
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>(std::min<int64_t>(steps, 65535), int64_t(sms) * kQkWarpsPerSm / p.S));
   const unsigned warps = static_cast<unsigned>(std::min<int64_t>(8, p.S));
   const dim3 grid(static_cast<unsigned>(std::min<int64_t>((p.S + warps - 1) / warps, int64_t(sms) * 2)),
                   static_cast<unsigned>(parts));
-  if (interleaved)
-    h3q::qk_norm_rope_kernel<G, true><<<grid, 32 * warps, 0, stream>>>(p);
-  else
-    h3q::qk_norm_rope_kernel<G, false><<<grid, 32 * warps, 0, stream>>>(p);
+  return launch_dependent(interleaved ? h3q::qk_norm_rope_kernel<G, true> : h3q::qk_norm_rope_kernel<G, false>, grid,
+                          32 * warps, 0, 0, stream, p);
 }
 
 // [rows, cols] bf16 row-major, boxes of 64 columns (128 bytes) x 128 rows,
@@ -631,10 +642,11 @@ static h3q_status fp8_quantize_any(bool weight, const void* x, int x_dtype, int6
     const int64_t blocks = (rows + h3q::kF8QuantRows - 1) / h3q::kF8QuantRows * ((KB + 1) / 2);
     if (blocks > INT32_MAX) return H3Q_ERR_UNSUPPORTED;
     const unsigned g = static_cast<unsigned>(blocks);
-    if (x_dtype == H3Q_DTYPE_BF16)
-      h3q::fp8_quantize_kernel<__nv_bfloat16><<<g, 256, 0, stream>>>(xb, rows, k, KB, codes, scales);
-    else
-      h3q::fp8_quantize_kernel<float><<<g, 256, 0, stream>>>(xf, rows, k, KB, codes, scales);
+    return x_dtype == H3Q_DTYPE_BF16
+               ? launch_dependent(h3q::fp8_quantize_kernel<__nv_bfloat16>, dim3(g), 256, 0, 0, stream, xb, rows, k, KB,
+                                  codes, scales)
+               : launch_dependent(h3q::fp8_quantize_kernel<float>, dim3(g), 256, 0, 0, stream, xf, rows, k, KB, codes,
+                                  scales);
   }
   return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
@@ -724,11 +736,10 @@ h3q_status h3q_qk_norm_rope(const void* q, const void* k, int64_t S, int64_t Hq,
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
   const bool il = interleaved != 0;
-  if (D <= 32) launch_qk<4>(p, il, sms, stream);
-  else if (D <= 64) launch_qk<8>(p, il, sms, stream);
-  else if (D <= 128) launch_qk<16>(p, il, sms, stream);
-  else launch_qk<32>(p, il, sms, stream);
-  return cudaGetLastError() == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+  if (D <= 32) return launch_qk<4>(p, il, sms, stream);
+  if (D <= 64) return launch_qk<8>(p, il, sms, stream);
+  if (D <= 128) return launch_qk<16>(p, il, sms, stream);
+  return launch_qk<32>(p, il, sms, stream);
 }
 
 struct AttLayout {

@@ -149,6 +149,12 @@ __device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t* bar, uint32_t p
   return __all_sync(0xFFFFFFFFu, mbar_wait_bounded_lazy(bar, parity, limit_ns, abort));
 }
 
+// Waits until the kernels before this one in the stream are done and their writes
+// visible. A kernel launched as a programmatic dependent may start while the last
+// blocks of the one before it still run, so that launch and set-up overlap; it reads
+// and writes no global memory before this.
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -166,6 +172,13 @@ __device__ __forceinline__ uint32_t cluster_map(const void* local, uint32_t rank
 // All threads of all CTAs of the cluster.
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// The same without ordering memory: for a cluster whose CTAs only have to have finished
+// reading one another's shared memory (the loads' values are in use). A release here
+// would wait for the output's stores.
+__device__ __forceinline__ void cluster_sync_relaxed() {
+  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
 }
 
 // Arrive on an mbarrier of any CTA of the cluster (release at cluster scope).
