@@ -226,10 +226,46 @@ h3q_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threa
   return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
 }
 
+// How the kernel for few tokens would run: CTAs per tile along K, and an estimate of its
+// time in microseconds.
+struct Fp8SmallPlan {
+  int splits;
+  bool two;  // two CTAs an SM
+  double us;
+};
+
+// Which fp8 product runs is decided by estimates from measured times of one K block of
+// one tile on one SM (pair), times the rounds over the SMs. Few tokens: 0.42 us up to 64
+// tokens a tile (two weight tiles a K block, SwiGLU: 0.60 from 64 tokens), 0.48 at 128
+// (SwiGLU 1.07), and 4 us for launch and ends (5.5 at 128), 1 more with a split K axis. The large kernel:
+// 0.50 us for its 256 x 256 tile of two SMs, and 5 us. Measured on both sides of the
+// border, for example: 256 tokens x 5376 x 5376 24.1 against 25.2 us, x 16128 48.1 against
+// 28.6; 128 x 16128 25.9 against 27.9; 512 x 14336 x 1024 19.6 against 56.8; 300 tokens,
+// SwiGLU 1360 -> 2176 13.7 against 11.9.
+constexpr double kF8LargeStepUs = 0.50, kF8LargeFixedUs = 5.0;
+
+template <int R, int TM>
+Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
+  constexpr double kStepUs = TM == 128 ? (R == 2 ? 1.07 : 0.48) : (R == 2 && TM == 64 ? 0.60 : 0.42);
+  const int64_t tiles = ((M + TM - 1) / TM) * ((N_out + 127) / 128);
+  const int64_t room = int64_t(sms) * (R * TM <= 64 ? 2 : 1);  // CTAs at once (registers)
+  Fp8SmallPlan pl{1, false, 0.0};
+  // Split the K axis while more CTAs fit and each keeps four K blocks. Clusters of eight
+  // leave SMs of a GPC over: they stop at three quarters of the room, and sit two to an SM
+  // from five eighths of the SMs on (128 tokens x 14336 x 1024: 24 us with one, 13 with two).
+  while (pl.splits < 8 && KB >= pl.splits * 8 && tiles * pl.splits * 2 <= (pl.splits == 4 ? room * 3 / 4 : room))
+    pl.splits *= 2;
+  pl.two = room > sms && tiles * pl.splits > (pl.splits == 8 ? sms * 5 / 8 : sms);
+  const int64_t rounds = (tiles * pl.splits + sms - 1) / sms;
+  pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs +
+          (TM == 128 ? 5.5 : 4.0) + (pl.splits > 1 ? 1.0 : 0.0);
+  return pl;
+}
+
 template <int EPI, int TM>
 h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w,
                                  const float* sw, int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
-                                 int sms, cudaStream_t stream) {
+                                 const Fp8SmallPlan& plan, cudaStream_t stream) {
   constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
   using Cfg = h3q::Fp8Small<R, TM>;
   CUtensorMap tw, tx;
@@ -250,14 +286,10 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   p.out = out;
   p.sh = sh;
   p.wait_limit_ns = g_wait_limit_ns.load();
-  // Split the K axis while another CTA an SM fits and each keeps at least four K blocks.
   const int64_t tiles = int64_t(p.num_m) * p.num_n;
-  const int resident = R * TM <= 64 ? 2 : 1;  // CTAs an SM (registers)
-  int splits = 1;
-  while (splits < 8 && tiles * splits * 2 <= int64_t(sms) * resident && p.KB >= splits * 2 * 4) splits *= 2;
+  const int splits = plan.splits;
   p.splits = splits;
-  const bool two = tiles * splits > sms && resident == 2;
-  const int room = (two ? 113 * 1024 : 226 * 1024) - Cfg::kFixed;
+  const int room = (plan.two ? 113 * 1024 : 226 * 1024) - Cfg::kFixed;
   p.stages = std::min(std::min(room / Cfg::kStage, h3q::kF8sMaxStages), std::max(3, (p.KB + splits - 1) / splits));
   const size_t smem = size_t(p.stages) * Cfg::kStage + Cfg::kFixed;
   return launch_dependent(h3q::gemm_fp8_small_kernel<EPI, TM>, dim3(static_cast<unsigned>(tiles * splits)),
@@ -307,25 +339,34 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
                           tout, p);
 }
 
-// Warps of qk_norm_rope wanted per SM: below that many tokens an SM, the heads of a
-// token are split over several warps.
-constexpr int kQkWarpsPerSm = 16;
-
-// At most this many tokens: the kernel for few tokens.
-constexpr int64_t kF8SmallTokens = 128;
-
 template <int EPI>
 h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w, const float* sw,
                            int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
                            cudaStream_t stream) {
+  constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
-  if (M > kF8SmallTokens) return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
-  if (M <= 16) return launch_gemm_fp8_small<EPI, 16>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
-  if (M <= 32) return launch_gemm_fp8_small<EPI, 32>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
-  if (M <= 64) return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
-  return launch_gemm_fp8_small<EPI, 128>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, sms, stream);
+  const int64_t KB = (K + 127) / 128;
+  if (M <= 16)
+    return launch_gemm_fp8_small<EPI, 16>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
+                                          plan_gemm_fp8_small<R, 16>(M, N_out, KB, sms), stream);
+  if (M <= 32)
+    return launch_gemm_fp8_small<EPI, 32>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
+                                          plan_gemm_fp8_small<R, 32>(M, N_out, KB, sms), stream);
+  const int64_t large_tiles = ((M + 255) / 256) * (R == 1 ? (N_out + 255) / 256 : N_out / 128);
+  const double large_us = double((large_tiles + sms / 2 - 1) / (sms / 2)) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs;
+  const Fp8SmallPlan p64 = plan_gemm_fp8_small<R, 64>(M, N_out, KB, sms);
+  const Fp8SmallPlan p128 = plan_gemm_fp8_small<R, 128>(M, N_out, KB, sms);
+  if (p64.us <= large_us && (M <= 64 || p64.us <= p128.us))
+    return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p64, stream);
+  if (M > 64 && p128.us <= large_us)
+    return launch_gemm_fp8_small<EPI, 128>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p128, stream);
+  return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
 }
+
+// Warps of qk_norm_rope wanted per SM: below that many tokens an SM, the heads of a
+// token are split over several warps.
+constexpr int kQkWarpsPerSm = 16;
 
 template <int G>
 h3q_status launch_qk(const h3q::QkParams& p, bool interleaved, int sms, cudaStream_t stream) {
