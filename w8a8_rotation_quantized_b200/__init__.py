@@ -339,7 +339,7 @@ def _t():
 
 def _is(t, dtype, shape, index):
     """t is a dense tensor of this dtype and shape on CUDA device `index`."""
-    return (t is not None and t.dtype is dtype and t.is_cuda and t.get_device() == index and t.shape == shape
+    return (t is not None and t.dtype is dtype and t.get_device() == index and t.shape == shape
             and t.is_contiguous())
 
 
@@ -348,8 +348,10 @@ def _run(name, fn, index, stream, *args):
     current stream."""
     torch = _t()
     if stream is None:
-        stream = torch.cuda.current_stream(index)
-    stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        stream = raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     if torch.cuda.current_device() == index:
         status = fn(*args, stream)
     else:
@@ -451,17 +453,19 @@ def h3q_qk_norm_rope(q, k, Hq, Hk, D, cos, sin, q_out, k_out, q_weight=None, k_w
     if q is None or q.dim() != 2 or not q.is_cuda:
         _need(w, "q", q, "bf16", (None, None), dense=False)
     S, index = q.shape[0], q.get_device()
-    lds = []
-    for name, t, heads in (("q", q, Hq), ("q_out", q_out, Hq), ("k", k, Hk), ("k_out", k_out, Hk)):
-        if heads == 0 and name[0] == "k":
-            lds.append(0)
-            continue
-        width = heads * D
-        if (t is None or t.dtype is not bf16 or t.dim() != 2 or t.get_device() != index or t.shape[0] != S
-                or t.shape[1] < width or (t.stride(1) != 1 and t.shape[1] > 1)):
-            _need(w, name, t, "bf16", (S, None), q.device, dense=False)
+
+    def ld(name, t, width):  # the row stride of a [S, >= width] bf16 view
+        if t is not None and t.dtype is bf16 and t.get_device() == index:
+            shape, stride = t.shape, t.stride()
+            if len(shape) == 2 and shape[0] == S and shape[1] >= width and stride[1] == 1:
+                return stride[0] if S > 1 else width  # the stride of a single row means nothing
+        _need(w, name, t, "bf16", (S, None), q.device, dense=False)
+        if t.shape[1] < width:
             raise ValueError(f"{w}: {name} must have at least {width} columns, got {t.shape[1]}")
-        lds.append(t.stride(0) if S > 1 else width)  # the stride of a single row means nothing
+        return t.stride(0) if S > 1 else width
+
+    ldq, ldqo = ld("q", q, Hq * D), ld("q_out", q_out, Hq * D)
+    ldk, ldko = (ld("k", k, Hk * D), ld("k_out", k_out, Hk * D)) if Hk else (0, 0)
     for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
         if t is not None and not _is(t, bf16, (D,), index):
             _need(w, name, t, "bf16", (D,), q.device)
@@ -475,9 +479,9 @@ def h3q_qk_norm_rope(q, k, Hq, Hk, D, cos, sin, q_out, k_out, q_weight=None, k_w
         raise ValueError(f"{w}: sin without cos")
     if positions is not None and not _is(positions, _t().int32, (S,), index):
         _need(w, "positions", positions, "i32", (S,), q.device)
-    _run(w, lib.h3q_qk_norm_rope, index, stream, q.data_ptr(), k.data_ptr() if Hk else None, S, Hq, Hk, D, lds[0],
-         lds[2], _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos), _ptr(sin), P, 2 * half, int(bool(interleaved)),
-         _ptr(positions), q_out.data_ptr(), k_out.data_ptr() if Hk else None, lds[1], lds[3])
+    _run(w, lib.h3q_qk_norm_rope, index, stream, q.data_ptr(), k.data_ptr() if Hk else None, S, Hq, Hk, D, ldq,
+         ldk, _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos), _ptr(sin), P, 2 * half, 1 if interleaved else 0,
+         _ptr(positions), q_out.data_ptr(), k_out.data_ptr() if Hk else None, ldqo, ldko)
 
 
 def h3q_gemm_s32(xq, wq, acc, stream=None) -> None:
