@@ -278,7 +278,9 @@ constexpr int kF8Warps = 16;                     // promotion warps
 constexpr int kF8Threads = 32 * kF8Warps + 128;  // then operand and scale producers, two MMA issuers
 constexpr int kF8Producer = kF8Warps, kF8Issuer = kF8Warps + 2;
 constexpr int kF8StageBytes = kAStage + kBStage;
-constexpr int kF8ScaleRing = 16;            // K blocks whose scales are in flight or waiting, handed over by fours
+constexpr int kF8ScaleRing = 16;            // K blocks whose scales are in flight or waiting ...
+constexpr int kF8ScaleGroup = 8;            // ... handed over in groups
+constexpr int kF8ScaleGroups = kF8ScaleRing / kF8ScaleGroup;
 constexpr int kF8ScaleSlot = 128 * 4 + 16;  // a K block's scales of the CTA's 128 rows, then of the two weight blocks
 constexpr int kF8OutTile = 32 * 64;         // a warp's 32 output rows of 64 bytes
 constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + kF8Warps * 2 * kF8OutTile + kF8ScaleRing * kF8ScaleSlot +
@@ -328,8 +330,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmOut, const Fp8Params p) {
   constexpr bool kSwi = EPI != kF8BF16;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // aligned by declaration, so that every address in it is a constant: the promotion
+  // warps have no registers for pointers
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sA = smem;
   uint8_t* sB = smem + kF8Stages * kAStage;
   uint8_t* out_tiles = sB + kF8Stages * kBStage;        // [warp][2]
@@ -341,7 +344,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   uint64_t* tempty = tfull + 2;
   uint64_t* drain = tempty + 2;
   uint64_t* rmax_bar = drain + 1;  // [quarter]: the four parts' row maxima are in shared memory
-  uint64_t* sfull = rmax_bar + 4;   // [group of four K blocks % 4]: the scales are in shared memory
+  uint64_t* sfull = rmax_bar + 4;   // [group % kF8ScaleGroups]: the group's scales are in shared memory
   uint64_t* sempty = sfull + 4;     // ... and have been read
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sempty + 4);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -436,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
       }
     } else if (warp == kF8Producer + 1) {
       // ------------------------------------------------------------ scales (both CTAs)
-      // Up to sixteen K blocks ahead, handed over by fours: each lane copies four rows'
+      // Up to sixteen K blocks ahead: each lane copies four rows'
       // (zeros past the end of M), lanes 0 and 1 the two weight blocks'.
       int n = 0;
       bool ok = true;
@@ -448,8 +451,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         const float* sw =
             p.sw + int64_t(kSwi ? ((lane & 1) ? p.b_row_up / 128 + nb : nb) : min(2 * nb + (lane & 1), p.last_nb)) * KB;
         for (int kb = 0; kb < KB; ++kb, ++n) {
-          if ((n & 3) == 0 &&
-              !mbar_wait_bounded_warp(&sempty[(n >> 2) & 3], ((n >> 4) & 1) ^ 1u, limit, abort_flag)) {
+          const int group = n / kF8ScaleGroup, slot = group & (kF8ScaleGroups - 1);
+          if (n % kF8ScaleGroup == 0 &&
+              !mbar_wait_bounded_warp(&sempty[slot], ((group / kF8ScaleGroups) & 1) ^ 1u, limit, abort_flag)) {
             ok = false;
             break;
           }
@@ -461,10 +465,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
           }
           if (lane < 2) cp_async4(dst + 512, sw + kb, true);
           sx += p.M;
-          if ((n & 3) == 3) cp_async_arrive(&sfull[(n >> 2) & 3]);
+          if (n % kF8ScaleGroup == kF8ScaleGroup - 1) cp_async_arrive(&sfull[slot]);
         }
       }
-      if (ok && (n & 3) != 0) cp_async_arrive(&sfull[(n >> 2) & 3]);
+      if (ok && n % kF8ScaleGroup != 0) cp_async_arrive(&sfull[n / kF8ScaleGroup & (kF8ScaleGroups - 1)]);
       cp_async_commit();
       cp_async_wait<0>();
     } else if (rank == 0) {
@@ -512,9 +516,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     uint8_t* out_tile = out_tiles + warp * 2 * kF8OutTile;
     const uint32_t my_scales = smem_u32(scale_ring) + row_in_cta * 4;
     const uint32_t block_scales = smem_u32(scale_ring) + 512;
+    // What the next K block needs is fetched behind the release of this one: its scales,
+    // and whether its products are there already (a wait costs some 200 cycles even when
+    // it need not wait).
+    const int total = pair < p.num_tiles ? (p.num_tiles - pair + npairs - 1) / npairs * KB : 0;
     int n = 0;  // K blocks so far: buffer n % 2, scale slot n % 16
     int iter = 0;
-    bool ok = true;
+    bool ready = false;
+    bool ok = total > 0 && mbar_wait_bounded_lazy(&sfull[0], 0, p.wait_limit_ns, abort_flag);
+    float sx_n = ok ? ld_shared_f32(my_scales) : 0.0f;
+    float2 sw_n = ok ? ld_shared_f32x2(block_scales) : make_float2(0.0f, 0.0f);
     for (int tile = pair; ok && tile < p.num_tiles; tile += npairs, ++iter) {
       float acc[2][32];
 #pragma unroll
@@ -522,16 +533,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
 #pragma unroll 1
-      for (int kb = 0; kb < KB; ++kb, ++n) {
-        if ((n & 3) == 0 && !mbar_wait_bounded_lazy(&sfull[(n >> 2) & 3], (n >> 4) & 1, p.wait_limit_ns, abort_flag)) {
-          ok = false;
-          break;
-        }
-        const uint32_t slot = (n & (kF8ScaleRing - 1)) * kF8ScaleSlot;
-        const float sxv = ld_shared_f32(my_scales + slot);
-        const float f0 = __fmul_rn(sxv, ld_shared_f32(block_scales + slot));
-        const float f1 = __fmul_rn(sxv, ld_shared_f32(block_scales + slot + 4));
-        if (!mbar_wait_bounded_lazy(&tfull[n & 1], (n >> 1) & 1, p.wait_limit_ns, abort_flag)) {
+      for (int kb = 0; kb < KB; ++kb) {
+        const float f0 = __fmul_rn(sx_n, sw_n.x), f1 = __fmul_rn(sx_n, sw_n.y);
+        if (!ready && !mbar_wait_bounded_lazy(&tfull[n & 1], (n >> 1) & 1, p.wait_limit_ns, abort_flag)) {
           ok = false;
           break;
         }
@@ -544,10 +548,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         tmem_ld32(ta + 128, r);
         tmem_ld_wait32(r);
         tc_fence_before();
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive_remote(tempty_leader + (n & 1) * 8);
-          if ((n & 3) == 3) mbar_arrive(&sempty[(n >> 2) & 3]);  // every lane has read the group's scales
+        if (lane == 0) mbar_arrive_remote(tempty_leader + (n & 1) * 8);  // the whole warp's loads are done
+        ++n;
+        if (n < total) {
+          if ((n & (kF8ScaleGroup - 1)) == 0) {
+            const int group = n / kF8ScaleGroup;
+            __syncwarp();  // every lane has read the last group's scales
+            if (lane == 0) mbar_arrive(&sempty[(group - 1) & (kF8ScaleGroups - 1)]);
+            if (!mbar_wait_bounded_lazy(&sfull[group & (kF8ScaleGroups - 1)], (group / kF8ScaleGroups) & 1,
+                                        p.wait_limit_ns, abort_flag)) {
+              ok = false;
+              break;
+            }
+          }
+          const uint32_t slot = (n & (kF8ScaleRing - 1)) * kF8ScaleSlot;
+          sx_n = ld_shared_f32(my_scales + slot);
+          sw_n = ld_shared_f32x2(block_scales + slot);
+          ready = mbar_test_wait(&tfull[n & 1], (n >> 1) & 1);
         }
         f8_promote(acc[1], r, f1);
       }
