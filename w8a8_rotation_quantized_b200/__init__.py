@@ -363,20 +363,21 @@ def _run(name, fn, index, stream, *args):
 
 def _fp8_quantizer(w, fn, x, codes, scales, weight, stream):
     torch = _t()
-    if x is not None and x.dim() == 2 and x.is_cuda:
-        rows, K = x.shape
-        index = x.get_device()
-        KB = (K + 127) // 128
-        dt = H3Q_DTYPE_BF16 if x.dtype is torch.bfloat16 else H3Q_DTYPE_F32
-        want = ((rows + 127) // 128, KB) if weight else (KB, rows)
-        if (_is(x, torch.bfloat16 if dt == H3Q_DTYPE_BF16 else torch.float32, (rows, K), index)
-                and _is(codes, torch.float8_e4m3fn, (rows, K), index) and _is(scales, torch.float32, want, index)):
-            return _run(w, fn, index, stream, x.data_ptr(), dt, rows, K, codes.data_ptr(), scales.data_ptr())
-    rows, K = _need(w, "w" if weight else "x", x, "bf16" if x is not None and x.dtype == torch.bfloat16 else "f32",
-                    (None, None)).shape
+    names = ("w", "wq", "sw") if weight else ("x", "xq", "sx")
+    kind = "bf16" if x is not None and x.dtype is torch.bfloat16 else "f32"
+    if x is None or x.dim() != 2 or not x.is_cuda or x.dtype not in (torch.bfloat16, torch.float32):
+        _need(w, names[0], x, kind, (None, None))
+    rows, K = x.shape
+    index = x.get_device()
     KB = (K + 127) // 128
-    _need(w, "wq" if weight else "xq", codes, "e4m3", (rows, K), x.device)
-    _need(w, "sw" if weight else "sx", scales, "f32", ((rows + 127) // 128, KB) if weight else (KB, rows), x.device)
+    shape = ((rows + 127) // 128, KB) if weight else (KB, rows)
+    if not (x.is_contiguous() and _is(codes, torch.float8_e4m3fn, (rows, K), index)
+            and _is(scales, torch.float32, shape, index)):
+        _need(w, names[0], x, kind, (None, None))
+        _need(w, names[1], codes, "e4m3", (rows, K), x.device)
+        _need(w, names[2], scales, "f32", shape, x.device)
+    _run(w, fn, index, stream, x.data_ptr(), H3Q_DTYPE_BF16 if kind == "bf16" else H3Q_DTYPE_F32, rows, K,
+         codes.data_ptr(), scales.data_ptr())
 
 
 def h3q_fp8_quantize(x, xq, sx, stream=None) -> None:

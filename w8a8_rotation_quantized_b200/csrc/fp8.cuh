@@ -523,7 +523,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     int n = 0;  // K blocks so far: buffer n % 2, scale slot n % 16
     int iter = 0;
     bool ready = false;
-    bool ok = total > 0 && mbar_wait_bounded_lazy(&sfull[0], 0, p.wait_limit_ns, abort_flag);
+    bool ok = total > 0 && mbar_wait_bounded_warp(&sfull[0], 0, p.wait_limit_ns, abort_flag);
     float sx_n = ok ? ld_shared_f32(my_scales) : 0.0f;
     float2 sw_n = ok ? ld_shared_f32x2(block_scales) : make_float2(0.0f, 0.0f);
     for (int tile = pair; ok && tile < p.num_tiles; tile += npairs, ++iter) {
@@ -535,7 +535,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 #pragma unroll 1
       for (int kb = 0; kb < KB; ++kb) {
         const float f0 = __fmul_rn(sx_n, sw_n.x), f1 = __fmul_rn(sx_n, sw_n.y);
-        if (!ready && !mbar_wait_bounded_lazy(&tfull[n & 1], (n >> 1) & 1, p.wait_limit_ns, abort_flag)) {
+        if (!__all_sync(0xFFFFFFFFu, ready) &&
+            !mbar_wait_bounded_warp(&tfull[n & 1], (n >> 1) & 1, p.wait_limit_ns, abort_flag)) {
           ok = false;
           break;
         }
@@ -555,7 +556,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
             const int group = n / kF8ScaleGroup;
             __syncwarp();  // every lane has read the last group's scales
             if (lane == 0) mbar_arrive(&sempty[(group - 1) & (kF8ScaleGroups - 1)]);
-            if (!mbar_wait_bounded_lazy(&sfull[group & (kF8ScaleGroups - 1)], (group / kF8ScaleGroups) & 1,
+            if (!mbar_wait_bounded_warp(&sfull[group & (kF8ScaleGroups - 1)], (group / kF8ScaleGroups) & 1,
                                         p.wait_limit_ns, abort_flag)) {
               ok = false;
               break;
@@ -596,7 +597,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
           maxima[part * 128] = amax;
           __syncwarp();
           if (lane == 0) mbar_arrive(&rmax_bar[quarter]);
-          if (!mbar_wait_bounded_lazy(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
+          if (!mbar_wait_bounded_warp(&rmax_bar[quarter], static_cast<uint32_t>(iter & 1), limit, abort_flag)) break;
 #pragma unroll
           for (int i = 0; i < 4; ++i) amax = max_nan(amax, maxima[i * 128]);
           float inv;
@@ -906,10 +907,10 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
 #pragma unroll 1
     for (int i = 0; i < nkb; ++i) {
       const int b = i % Cfg::kBufs;
-      if ((i & 3) == 0 && !mbar_wait_bounded_lazy(&sfull[(i >> 2) & 3], (i >> 4) & 1, limit, abort_flag)) break;
+      if ((i & 3) == 0 && !mbar_wait_bounded_warp(&sfull[(i >> 2) & 3], (i >> 4) & 1, limit, abort_flag)) break;
       const uint32_t slot = smem_u32(scale_ring) + (i & (kF8sScaleRing - 1)) * Cfg::kScaleSlot;
       const float swv = ld_shared_f32(slot + sw_at);
-      if (!mbar_wait_bounded_lazy(&tfull[b], (i / Cfg::kBufs) & 1, limit, abort_flag)) break;
+      if (!mbar_wait_bounded_warp(&tfull[b], (i / Cfg::kBufs) & 1, limit, abort_flag)) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < Cfg::kHalf / kChunk; ++c) {
