@@ -551,23 +551,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         tc_fence_before();
         if (lane == 0) mbar_arrive_remote(tempty_leader + (n & 1) * 8);  // the whole warp's loads are done
         ++n;
-        if (n < total) {
-          if ((n & (kF8ScaleGroup - 1)) == 0) {
-            const int group = n / kF8ScaleGroup;
-            __syncwarp();  // every lane has read the last group's scales
-            if (lane == 0) mbar_arrive(&sempty[(group - 1) & (kF8ScaleGroups - 1)]);
-            if (!mbar_wait_bounded_warp(&sfull[group & (kF8ScaleGroups - 1)], (group / kF8ScaleGroups) & 1,
-                                        p.wait_limit_ns, abort_flag)) {
-              ok = false;
-              break;
-            }
+        const bool more = n < total;
+        if (more && (n & (kF8ScaleGroup - 1)) == 0) {
+          const int group = n / kF8ScaleGroup;
+          __syncwarp();  // every lane has read the last group's scales
+          if (lane == 0) mbar_arrive(&sempty[(group - 1) & (kF8ScaleGroups - 1)]);
+          if (!mbar_wait_bounded_warp(&sfull[group & (kF8ScaleGroups - 1)], (group / kF8ScaleGroups) & 1,
+                                      p.wait_limit_ns, abort_flag)) {
+            ok = false;
+            break;
           }
+        }
+        f8_promote(acc[1], r, f1);
+        if (more) {
           const uint32_t slot = (n & (kF8ScaleRing - 1)) * kF8ScaleSlot;
           sx_n = ld_shared_f32(my_scales + slot);
           sw_n = ld_shared_f32x2(block_scales + slot);
           ready = mbar_test_wait(&tfull[n & 1], (n >> 1) & 1);
         }
-        f8_promote(acc[1], r, f1);
       }
       if (!ok) break;
       int mb, nb;
