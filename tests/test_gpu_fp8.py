@@ -222,6 +222,24 @@ def test_swiglu_within_bound(h3q, cuda_device, M, K, F, with_bias):
     _close(back, h, e + half_step * (1 + 2.0 ** -20) + 2.0 ** -126)
 
 
+# the K axis split over two to eight CTAs, token tiles of every size, and several output
+# tiles for each SM pair with an odd number of K blocks
+LONG_SHAPES = [(1, 14336, 1024), (9, 14336, 1000), (30, 14336, 1024), (60, 14336, 1016), (100, 14336, 1024),
+               (256, 14336, 1024), (512, 14336, 520), (1, 5376, 5376), (20, 5376, 5376), (70, 5376, 5376),
+               (192, 5376, 2688), (40, 784, 5000), (5000, 400, 3000), (6000, 1040, 4104), (2100, 2064, 5384)]
+
+
+@pytest.mark.parametrize("M,K,N", LONG_SHAPES)
+def test_linear_over_split_and_many_tiles(h3q, cuda_device, M, K, N):
+    test_linear_within_bound(h3q, cuda_device, M, K, N)
+
+
+@pytest.mark.parametrize("M,K,F", [(1, 14336, 128), (10, 14336, 640), (32, 5376, 2176), (33, 14336, 512), (128, 14336, 384),
+                                   (3000, 656, 2560), (3001, 1040, 2688)])
+def test_swiglu_over_split_and_many_tiles(h3q, cuda_device, M, K, F):
+    test_swiglu_within_bound(h3q, cuda_device, M, K, F, M % 2 == 0)
+
+
 def test_scales_of_any_value_are_applied(h3q, cuda_device):
     """Negative, zero, huge and tiny scales, all codes: the product is what the operands say."""
     M, K, N = 70, 400, 264

@@ -245,7 +245,8 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
 // silu(g) = g / (1 + e^-g) from the hardware's 2^x and reciprocal approximations
 // (relative error about 2^-21 + |g| 2^-24, far below the bf16 or e4m3 rounding that
 // follows: e^-g is 2^x of a rounded product).
-// Below g = -88.7, e^-g overflows and the result is -0; silu is under 2^-121 there.
+// Below g = -87.3 the reciprocal leaves the normal range and the result is -0; silu is
+// above -2^-119 there.
 __device__ __forceinline__ float silu_approx(float g) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(__fmul_rn(g, -1.44269504f)));

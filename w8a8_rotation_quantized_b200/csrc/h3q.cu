@@ -237,28 +237,40 @@ struct Fp8SmallPlan {
 // Which fp8 product runs is decided by estimates from measured times of one K block of
 // one tile on one SM (pair), times the rounds over the SMs. Few tokens: 0.42 us up to 64
 // tokens a tile (two weight tiles a K block, SwiGLU: 0.60 from 64 tokens), 0.48 at 128
-// (SwiGLU 1.07), and 4 us for launch and ends (5.5 at 128), 1 more with a split K axis. The large kernel:
-// 0.50 us for its 256 x 256 tile of two SMs, and 5 us. Measured on both sides of the
-// border, for example: 256 tokens x 5376 x 5376 24.1 against 25.2 us, x 16128 48.1 against
-// 28.6; 128 x 16128 25.9 against 27.9; 512 x 14336 x 1024 19.6 against 56.8; 300 tokens,
-// SwiGLU 1360 -> 2176 13.7 against 11.9.
-constexpr double kF8LargeStepUs = 0.50, kF8LargeFixedUs = 5.0;
+// (SwiGLU 1.07), 4 us for launch and ends (5.5 with 128 rows of sums to hand over), 1 more
+// with a split K axis. The large kernel: 0.45 us for its 256 x 256 tile of two SMs, and 5
+// us. Measured on both sides of the border, for example (us, few tokens against large):
+// 64 x 5376 x 5376 14.2, 24.2; 512 x 14336 x 1024 19.6, 56.8; 256 x 5376 x 16128 48.1,
+// 28.6; SwiGLU 128 x 1360 -> 2176 9.8, 11.5; 384 x 1360 -> 2176 14.5, 12.0.
+constexpr double kF8LargeStepUs = 0.45, kF8LargeFixedUs = 5.0;
 
 template <int R, int TM>
 Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
   constexpr double kStepUs = TM == 128 ? (R == 2 ? 1.07 : 0.48) : (R == 2 && TM == 64 ? 0.60 : 0.42);
   const int64_t tiles = ((M + TM - 1) / TM) * ((N_out + 127) / 128);
-  const int64_t room = int64_t(sms) * (R * TM <= 64 ? 2 : 1);  // CTAs at once (registers)
+  // Split the K axis as far as the CTAs find room and two K blocks are left to each (four
+  // with eight CTAs): up to seven quarters of the SMs where two CTAs fit an SM
+  // (registers) and each reads a single weight tile a K block, else one CTA an SM. A
+  // cluster sits in one GPC, so the larger it is the more SMs stay over: what still fitted
+  // was seven eighths of the SMs for three and four, two thirds for six and eight (four
+  // thirds at two an SM); past it a launch takes a second round (24 clusters of six: 30 us
+  // instead of 18). One token, K 5376, in a graph: N 5376 split six ways 10.4 us, four
+  // 11.0, not 19.1; N 16128 two 20.3, not 21.4; SwiGLU to 14336 not 28.7, two 29.3.
+  const bool fits_two = R * TM <= 64;
   Fp8SmallPlan pl{1, false, 0.0};
-  // Split the K axis while more CTAs fit and each keeps four K blocks. Clusters of eight
-  // leave SMs of a GPC over: they stop at three quarters of the room, and sit two to an SM
-  // from five eighths of the SMs on (128 tokens x 14336 x 1024: 24 us with one, 13 with two).
-  while (pl.splits < 8 && KB >= pl.splits * 8 && tiles * pl.splits * 2 <= (pl.splits == 4 ? room * 3 / 4 : room))
-    pl.splits *= 2;
-  pl.two = room > sms && tiles * pl.splits > (pl.splits == 8 ? sms * 5 / 8 : sms);
+  for (const int s : {2, 3, 4, 6, 8}) {
+    int64_t most = fits_two ? (s == 8 ? int64_t(sms) * 4 / 3 : int64_t(sms) * 7 / 4)
+                            : (s == 2 ? int64_t(sms) : s <= 4 ? int64_t(sms) * 7 / 8 : int64_t(sms) * 2 / 3);
+    if (R == 2 && most > sms) most = sms;
+    if (tiles * s <= most && KB >= (s == 8 ? 4 : 2) * s) pl.splits = s;
+  }
+  // Half of an SM's shared memory for the ring where two CTAs fit, so that the next
+  // launch's find room beside this one's; all of it for the long streams of an unsplit
+  // gate/up product (28.7 against 30.4 us).
+  pl.two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
   const int64_t rounds = (tiles * pl.splits + sms - 1) / sms;
   pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs +
-          (TM == 128 ? 5.5 : 4.0) + (pl.splits > 1 ? 1.0 : 0.0);
+          (R * TM >= 128 ? 5.5 : 4.0) + (pl.splits > 1 ? 1.0 : 0.0);
   return pl;
 }
 
