@@ -325,14 +325,18 @@ def h3q_attention_prep(q, k, v, H, qq, qs, kq, ks, vt, stream=None) -> None:
 # The fp8 and query/key calls are also made for single tokens, where the checks of their
 # operands would cost more than the kernel: they test each operand in one expression and
 # come to the checks above only to name the fault.
-_torch = None
+_torch = _raw_stream = _current_device = None
 
 
 def _t():
     """torch, imported on first use."""
-    global _torch
+    global _torch, _raw_stream, _current_device
     if _torch is None:
         import torch
+        # the handles without the Stream object around them, where this torch has them
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda index: torch.cuda.current_stream(index).cuda_stream)
+        _current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
         _torch = torch
     return _torch
 
@@ -343,19 +347,28 @@ def _is(t, dtype, shape, index):
             and t.is_contiguous())
 
 
+def _row_stride(t, dtype, S, width, index):
+    """The row stride of t if it is a [S, >= width] view of this dtype with unit column
+    stride on CUDA device `index` (of a single row, whose stride means nothing, its width);
+    else None."""
+    if t is not None and t.dtype is dtype and t.get_device() == index:
+        shape, stride = t.shape, t.stride()
+        if len(shape) == 2 and shape[0] == S and shape[1] >= width and stride[1] == 1:
+            return stride[0] if S > 1 else width
+    return None
+
+
 def _run(name, fn, index, stream, *args):
     """Calls fn(*args, stream) with CUDA device `index` current, on `stream` or that device's
     current stream."""
-    torch = _t()
     if stream is None:
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        stream = raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
+        stream = _raw_stream(index)
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if torch.cuda.current_device() == index:
+    if _current_device() == index:
         status = fn(*args, stream)
     else:
-        with torch.cuda.device(index):
+        with _t().cuda.device(index):
             status = fn(*args, stream)
     if status != H3Q_OK:
         raise H3QError(status, name)
@@ -450,39 +463,48 @@ def h3q_qk_norm_rope(q, k, Hq, Hk, D, cos, sin, q_out, k_out, q_weight=None, k_w
     Hk = 0), then the rotation by row positions[t] (int32 [S]; None: row t) of cos, sin
     (fp32 [P, rot/2]; None: no rotation). q_out, k_out: the same shapes, may be q and k."""
     w = "h3q_qk_norm_rope"
-    bf16, f32 = _t().bfloat16, _t().float32
+    torch = _t()
+    bf16, f32 = torch.bfloat16, torch.float32
     if q is None or q.dim() != 2 or not q.is_cuda:
         _need(w, "q", q, "bf16", (None, None), dense=False)
     S, index = q.shape[0], q.get_device()
-
-    def ld(name, t, width):  # the row stride of a [S, >= width] bf16 view
-        if t is not None and t.dtype is bf16 and t.get_device() == index:
-            shape, stride = t.shape, t.stride()
-            if len(shape) == 2 and shape[0] == S and shape[1] >= width and stride[1] == 1:
-                return stride[0] if S > 1 else width  # the stride of a single row means nothing
-        _need(w, name, t, "bf16", (S, None), q.device, dense=False)
-        if t.shape[1] < width:
-            raise ValueError(f"{w}: {name} must have at least {width} columns, got {t.shape[1]}")
-        return t.stride(0) if S > 1 else width
-
-    ldq, ldqo = ld("q", q, Hq * D), ld("q_out", q_out, Hq * D)
-    ldk, ldko = (ld("k", k, Hk * D), ld("k_out", k_out, Hk * D)) if Hk else (0, 0)
-    for name, t in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if t is not None and not _is(t, bf16, (D,), index):
-            _need(w, name, t, "bf16", (D,), q.device)
+    ldq, ldqo = _row_stride(q, bf16, S, Hq * D, index), _row_stride(q_out, bf16, S, Hq * D, index)
+    ldk = ldko = 0
+    if Hk:
+        ldk, ldko = _row_stride(k, bf16, S, Hk * D, index), _row_stride(k_out, bf16, S, Hk * D, index)
+    if ldq is None or ldqo is None or ldk is None or ldko is None:
+        views = [("q", q, Hq), ("q_out", q_out, Hq)] + ([("k", k, Hk), ("k_out", k_out, Hk)] if Hk else [])
+        for name, t, heads in views:
+            _need(w, name, t, "bf16", (S, None), q.device, dense=False)
+            if t.shape[1] < heads * D:
+                raise ValueError(f"{w}: {name} must have at least {heads * D} columns, got {t.shape[1]}")
+        raise ValueError(f"{w}: q, q_out, k and k_out must be [S, columns] views with unit column stride")
+    qw = kw = c = s = at = None  # optional operands' pointers
     P = half = 0
+    if q_weight is not None:
+        if not _is(q_weight, bf16, (D,), index):
+            _need(w, "q_weight", q_weight, "bf16", (D,), q.device)
+        qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if not _is(k_weight, bf16, (D,), index):
+            _need(w, "k_weight", k_weight, "bf16", (D,), q.device)
+        kw = k_weight.data_ptr()
     if cos is not None:
-        if not (cos.dim() == 2 and _is(cos, f32, cos.shape, index) and _is(sin, f32, cos.shape, index)):
-            P, half = _need(w, "cos", cos, "f32", (None, None), q.device).shape
-            _need(w, "sin", sin, "f32", (P, half), q.device)
-        P, half = cos.shape
+        shape = cos.shape
+        if len(shape) != 2 or not (_is(cos, f32, shape, index) and _is(sin, f32, shape, index)):
+            _need(w, "cos", cos, "f32", (None, None), q.device)
+            _need(w, "sin", sin, "f32", tuple(shape), q.device)
+        P, half = shape
+        c, s = cos.data_ptr(), sin.data_ptr()
     elif sin is not None:
         raise ValueError(f"{w}: sin without cos")
-    if positions is not None and not _is(positions, _t().int32, (S,), index):
-        _need(w, "positions", positions, "i32", (S,), q.device)
-    _run(w, lib.h3q_qk_norm_rope, index, stream, q.data_ptr(), k.data_ptr() if Hk else None, S, Hq, Hk, D, ldq,
-         ldk, _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos), _ptr(sin), P, 2 * half, 1 if interleaved else 0,
-         _ptr(positions), q_out.data_ptr(), k_out.data_ptr() if Hk else None, ldqo, ldko)
+    if positions is not None:
+        if not _is(positions, torch.int32, (S,), index):
+            _need(w, "positions", positions, "i32", (S,), q.device)
+        at = positions.data_ptr()
+    _run(w, lib.h3q_qk_norm_rope, index, stream, q.data_ptr(), k.data_ptr() if Hk else None, S, Hq, Hk, D, ldq, ldk,
+         qw, kw, eps, c, s, P, 2 * half, 1 if interleaved else 0, at, q_out.data_ptr(),
+         k_out.data_ptr() if Hk else None, ldqo, ldko)
 
 
 def h3q_gemm_s32(xq, wq, acc, stream=None) -> None:
