@@ -673,8 +673,9 @@ struct Fp8Small {
   static constexpr int kStage = R * 128 * 128 + TM * 128;
   static constexpr int kCols = R * TM;                       // tensor-memory columns of one K block
   static constexpr int kHalf = kCols / 2;                    // columns of a promotion thread
-  static constexpr int kBufs = kCols >= 256 ? 2 : 4;
-  static constexpr int kTmem = kCols * kBufs < 32 ? 32 : kCols * kBufs;
+  static constexpr int kBufs = kCols > 128 ? 2 : 4;
+  // tensor memory is allocated by powers of two
+  static constexpr int kTmem = kCols * kBufs <= 64 ? 64 : kCols * kBufs <= 128 ? 128 : kCols * kBufs <= 256 ? 256 : 512;
   static constexpr int kPartials = R * TM * 128 * 4;
   static_assert(kPartials <= 3 * kStage, "the partial sums fit in the operand ring");
   static constexpr int kScaleSlot = TM * 4 + 16;
@@ -900,7 +901,7 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
     // gate or up, else half of the tokens.
     const int half = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
-    constexpr int kChunk = Cfg::kHalf < 32 ? Cfg::kHalf : 32;
+    constexpr int kChunk = Cfg::kHalf % 32 == 0 ? 32 : Cfg::kHalf % 16 == 0 ? 16 : 8;
     float2 acc[Cfg::kHalf / 2];
 #pragma unroll
     for (int m = 0; m < Cfg::kHalf / 2; ++m) acc[m] = make_float2(0.0f, 0.0f);

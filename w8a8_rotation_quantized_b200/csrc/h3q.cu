@@ -236,17 +236,20 @@ struct Fp8SmallPlan {
 
 // Which fp8 product runs is decided by estimates from measured times of one K block of
 // one tile on one SM (pair), times the rounds over the SMs. Few tokens: 0.42 us up to 64
-// tokens a tile (two weight tiles a K block, SwiGLU: 0.60 from 64 tokens), 0.48 at 128
-// (SwiGLU 1.07), 4 us for launch and ends (5.5 with 128 rows of sums to hand over), 1 more
-// with a split K axis. The large kernel: 0.45 us for its 256 x 256 tile of two SMs, and 5
-// us. Measured on both sides of the border, for example (us, few tokens against large):
+// tokens a tile (two weight tiles a K block, SwiGLU: 0.60 from 48 tokens), 0.45 at 96
+// (SwiGLU 0.70), 0.48 at 128 (SwiGLU 1.07); 4 us for launch and ends (5.5 with 96 or more
+// rows of sums to hand over), 1 more with a split K axis, 2.5 more with large clusters
+// that share their SMs. The large kernel: 0.45 us for its 256 x 256 tile of two SMs, and
+// 5 us. Measured on both sides of the border, for example (us, few tokens against large):
 // 64 x 5376 x 5376 14.2, 24.2; 512 x 14336 x 1024 19.6, 56.8; 256 x 5376 x 16128 48.1,
 // 28.6; SwiGLU 128 x 1360 -> 2176 9.8, 11.5; 384 x 1360 -> 2176 14.5, 12.0.
 constexpr double kF8LargeStepUs = 0.45, kF8LargeFixedUs = 5.0;
 
 template <int R, int TM>
 Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
-  constexpr double kStepUs = TM == 128 ? (R == 2 ? 1.07 : 0.48) : (R == 2 && TM == 64 ? 0.60 : 0.42);
+  constexpr double kStepUs = TM == 128  ? (R == 2 ? 1.07 : 0.48)
+                             : TM == 96 ? (R == 2 ? 0.70 : 0.45)
+                                        : (R == 2 && TM >= 48 ? 0.60 : 0.42);
   const int64_t tiles = ((M + TM - 1) / TM) * ((N_out + 127) / 128);
   // Split the K axis as far as the CTAs find room and two K blocks are left to each (four
   // with eight CTAs): up to seven quarters of the SMs where two CTAs fit an SM
@@ -270,7 +273,8 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
   pl.two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
   const int64_t rounds = (tiles * pl.splits + sms - 1) / sms;
   pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs +
-          (R * TM >= 128 ? 5.5 : 4.0) + (pl.splits > 1 ? 1.0 : 0.0);
+          (R * TM >= 96 ? 5.5 : 4.0) + (pl.splits > 1 ? 1.0 : 0.0) +
+          (TM == 64 && pl.splits >= 6 ? 2.5 : 0.0);
   return pl;
 }
 
@@ -365,14 +369,22 @@ h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t
   if (M <= 32)
     return launch_gemm_fp8_small<EPI, 32>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
                                           plan_gemm_fp8_small<R, 32>(M, N_out, KB, sms), stream);
+  if (M <= 48)
+    return launch_gemm_fp8_small<EPI, 48>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
+                                          plan_gemm_fp8_small<R, 48>(M, N_out, KB, sms), stream);
   const int64_t large_tiles = ((M + 255) / 256) * (R == 1 ? (N_out + 255) / 256 : N_out / 128);
   const double large_us = double((large_tiles + sms / 2 - 1) / (sms / 2)) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs;
   const Fp8SmallPlan p64 = plan_gemm_fp8_small<R, 64>(M, N_out, KB, sms);
+  const Fp8SmallPlan p96 = plan_gemm_fp8_small<R, 96>(M, N_out, KB, sms);
   const Fp8SmallPlan p128 = plan_gemm_fp8_small<R, 128>(M, N_out, KB, sms);
-  if (p64.us <= large_us && (M <= 64 || p64.us <= p128.us))
-    return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p64, stream);
-  if (M > 64 && p128.us <= large_us)
+  const double least = M <= 64 ? p64.us : std::min(std::min(p64.us, p96.us), p128.us);
+  if (least <= large_us) {
+    if (least == p64.us)
+      return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p64, stream);
+    if (least == p96.us)
+      return launch_gemm_fp8_small<EPI, 96>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p96, stream);
     return launch_gemm_fp8_small<EPI, 128>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p128, stream);
+  }
   return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
 }
 
