@@ -81,14 +81,15 @@ __device__ __forceinline__ float fp8_absmax8(const float (&v)[8]) {
 }
 
 __device__ __forceinline__ uint2 fp8_codes8(const float (&v)[8], float inv) {
-  float t[8];
+  float2 t[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) t[i] = __fmul_rn(v[i], inv);
-  return make_uint2(f32x4_to_e4m3x4(t[0], t[1], t[2], t[3]), f32x4_to_e4m3x4(t[4], t[5], t[6], t[7]));
+  for (int i = 0; i < 4; ++i) t[i] = __fmul2_rn(make_float2(v[2 * i], v[2 * i + 1]), make_float2(inv, inv));
+  return make_uint2(f32x4_to_e4m3x4(t[0].x, t[0].y, t[1].x, t[1].y), f32x4_to_e4m3x4(t[2].x, t[2].y, t[3].x, t[3].y));
 }
 
-// Eight consecutive elements as loaded, the largest magnitude among them, and their
-// codes. bf16 magnitudes compare as packed pairs; a NaN wins.
+// Eight consecutive elements as loaded; the bits of the largest magnitude among them (of
+// a bf16 pair's two halves, compared side by side), which max_bits combines and top turns
+// into the magnitude; and their codes. A NaN wins.
 template <typename T>
 struct Fp8Chunk;
 
@@ -99,18 +100,18 @@ struct Fp8Chunk<__nv_bfloat16> {
     const uint4 a = __ldcs(reinterpret_cast<const uint4*>(p));
     w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w;
   }
-  __device__ __forceinline__ float absmax16() const {  // over the sixteen lanes that share a block
-    auto two = [](uint32_t u) { return *reinterpret_cast<const __nv_bfloat162*>(&u); };
-    __nv_bfloat162 m = two(w[0] & 0x7FFF7FFFu);
+  static __device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float top(uint32_t bits) {
+    return max_nan(__uint_as_float(bits << 16), __uint_as_float(bits & 0xFFFF0000u));
+  }
+  __device__ __forceinline__ uint32_t absmax() const {
+    uint32_t m = w[0] & 0x7FFF7FFFu;
 #pragma unroll
-    for (int i = 1; i < 4; ++i) m = __hmax2_nan(m, two(w[i] & 0x7FFF7FFFu));
-    uint32_t u = *reinterpret_cast<const uint32_t*>(&m);
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) {
-      m = __hmax2_nan(two(u), two(__shfl_xor_sync(0xFFFFFFFFu, u, o)));
-      u = *reinterpret_cast<const uint32_t*>(&m);
-    }
-    return max_nan(__uint_as_float(u << 16), __uint_as_float(u & 0xFFFF0000u));
+    for (int i = 1; i < 4; ++i) m = max_bits(m, w[i] & 0x7FFF7FFFu);
+    return m;
   }
   __device__ __forceinline__ uint2 codes(float inv) const {
     float v[8];
@@ -131,19 +132,20 @@ struct Fp8Chunk<float> {
     v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
-  __device__ __forceinline__ float absmax16() const {
-    float a = fp8_absmax8(v);
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) a = max_nan(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
-    return a;
+  static __device__ __forceinline__ uint32_t max_bits(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
   }
+  static __device__ __forceinline__ float top(uint32_t bits) { return __uint_as_float(bits); }
+  __device__ __forceinline__ uint32_t absmax() const { return __float_as_uint(fp8_absmax8(v)); }
   __device__ __forceinline__ uint2 codes(float inv) const { return fp8_codes8(v, inv); }
 };
 
 // 1 x 128 blocks. A CTA takes 32 rows x 256 columns, a warp four of the rows: sixteen
-// lanes a block, eight elements each, all four loads in flight at once. The scales of
-// the 32 rows leave together, a line for each of the two K blocks. Bound by memory
-// (264 MB for 16384 x 5376 bf16).
+// lanes a block, eight elements each, all four loads in flight at once. The four rows'
+// maxima are combined together, each exchange halving the rows a lane still carries, so
+// that every lane ends with one of its block's four scales and divides once (five
+// exchanges for four rows; with four each, and four divisions, the kernel was issue
+// bound). The scales of the 32 rows leave together, a line for each of the two K blocks.
 constexpr int kF8QuantRows = 32;
 
 template <typename T>
@@ -156,20 +158,32 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int col = kb * 128 + 8 * lane;
   const int64_t m0 = int64_t(rb) * kF8QuantRows;
+  const int64_t first = (m0 + 4 * warp) * K + col;
+  const int rows = col < K ? static_cast<int>(min(int64_t(4), M - m0 - 4 * warp)) : 0;  // of this warp, may be negative
   grid_dependency_wait();
   Fp8Chunk<T> v[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + 4 * warp + i;
-    if (m < M && col < K) v[i].load(x + m * K + col);
-  }
+  for (int i = 0; i < 4; ++i)
+    if (i < rows) v[i].load(x + first + int64_t(i) * K);
+  uint32_t k[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) k[i] = v[i].absmax();
+  auto exchange = [](uint32_t keep, uint32_t give, int mask) {
+    return Fp8Chunk<T>::max_bits(keep, __shfl_xor_sync(0xFFFFFFFFu, give, mask));
+  };
+  const bool b3 = lane & 8, b2 = lane & 4;
+  const uint32_t k0 = exchange(b3 ? k[2] : k[0], b3 ? k[0] : k[2], 8);  // row 0 or 2
+  const uint32_t k1 = exchange(b3 ? k[3] : k[1], b3 ? k[1] : k[3], 8);  // row 1 or 3
+  uint32_t top = exchange(b2 ? k1 : k0, b2 ? k0 : k1, 4);
+  top = exchange(top, top, 2);
+  top = exchange(top, top, 1);
+  float inv;
+  const float s = fp8_scale(Fp8Chunk<T>::top(top), inv);  // of row (lane >> 2) & 3
+  if ((lane & 3) == 0) scales[lane >> 4][4 * warp + ((lane >> 2) & 3)] = s;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int64_t m = m0 + 4 * warp + i;
-    float inv;
-    const float s = fp8_scale(v[i].absmax16(), inv);
-    if (m < M && col < K) *reinterpret_cast<uint2*>(codes + m * K + col) = v[i].codes(inv);
-    if ((lane & 15) == 0) scales[lane >> 4][4 * warp + i] = s;
+    const float inv_i = __shfl_sync(0xFFFFFFFFu, inv, (lane & 16) | (4 * i));
+    if (i < rows) *reinterpret_cast<uint2*>(codes + first + int64_t(i) * K) = v[i].codes(inv_i);
   }
   __syncthreads();
   if (warp < 2 && kb + warp < KB && m0 + lane < M) sx[int64_t(kb + warp) * M + m0 + lane] = scales[warp][lane];
