@@ -9,13 +9,14 @@
 // one token at a time, so its lanes load the token's table row once for all of its
 // heads and fold the norm's weights into it: with C_i = w_i c_i and S_i = -+w_p s_i (p
 // the partner of i), the result is r (x_i C_i + x_p S_i), three operations an element.
-// Eight heads a lane group are in flight at once (two blocks an SM: 129 us at 84 heads
-// of 128 over 16384 tokens; four in flight 149, four at three or four blocks 135-143).
-// The kernel reads and writes every element once and is bound by memory: 704 MB there,
-// 83% of the copy rate. Few tokens are spread over more warps by splitting the heads.
+// Six heads a lane group are worked on while the next six load (two blocks an SM: 114 us
+// at 84 heads of 128 over 16384 tokens; eight at once without loads ahead 124, four 149,
+// three or more blocks 120 to 135). Every element is read and written once and memory is
+// the bound: 713 MB there, 95% of the measured copy rate. Few tokens are spread over more
+// warps by splitting the heads.
 //
-// Each lane holds its elements until they are stored, and a group's loads come
-// before its stores, so q_out and k_out may be q and k themselves.
+// A head's loads come before its stores and no head reads another's elements, so q_out
+// and k_out may be q and k themselves.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -53,7 +54,7 @@ __device__ __forceinline__ void qk_load8(const __nv_bfloat16* p, float (&v)[8]) 
 template <int G, bool INTER>
 __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) {
   constexpr int kHeads = 32 / G;  // heads a warp step takes
-  constexpr int kUnroll = 8;      // steps in flight
+  constexpr int kUnroll = 6;      // steps worked on, and as many in flight
   const int lane = threadIdx.x & 31;
   const int l = lane % G, sub = lane / G;
   const bool live = 8 * l < p.D;
@@ -124,14 +125,21 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
           sw[i] = __fmul2_rn(sw[i], INTER ? make_float2(wp[2 * i + 1], wp[2 * i]) : make_float2(wp[2 * i], wp[2 * i + 1]));
         }
       }
-      for (int st = lo; st < hi; st += kUnroll) {
-        uint4 raw[kUnroll];
+      uint4 next[kUnroll];
+      auto fetch = [&](int st) {
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           const int h = (st + u) * kHeads + sub;
-          raw[u] = make_uint4(0u, 0u, 0u, 0u);
-          if (st + u < hi && live && h < H) raw[u] = *reinterpret_cast<const uint4*>(src + int64_t(h) * p.D);
+          next[u] = make_uint4(0u, 0u, 0u, 0u);
+          if (st + u < hi && live && h < H) next[u] = *reinterpret_cast<const uint4*>(src + int64_t(h) * p.D);
         }
+      };
+      fetch(lo);
+      for (int st = lo; st < hi; st += kUnroll) {
+        uint4 raw[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) raw[u] = next[u];
+        if (st + kUnroll < hi) fetch(st + kUnroll);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
           if (st + u >= hi) break;  // the same for the whole warp
