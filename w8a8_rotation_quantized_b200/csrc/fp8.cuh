@@ -310,6 +310,7 @@ struct Fp8Params {
   int M, N, K;              // N: output columns (SwiGLU: F)
   int KB;                   // K blocks: ceil(K / 128)
   int num_m, num_n, num_tiles, group_m;
+  float inv_per_group, inv_group_m;  // 1 / (group_m num_n), 1 / group_m
   int b_row_up;             // SwiGLU: first up row of the weight (= F)
   int last_nb;              // last row of sw
   const float* sx;          // [KB, M]
@@ -403,14 +404,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
   grid_dependency_wait();
 
+  // Tiles run down groups of group_m row blocks, as in the int8 GEMM. The quotients come
+  // from a product with the reciprocal and one correction, exact below 2^23 tiles (more
+  // would be a terabyte of output): an integer division here costs more than a K block.
+  auto quotient = [](int n, int d, float inv) {
+    int q = static_cast<int>(__fmul_rn(static_cast<float>(n), inv));
+    const int r = n - q * d;
+    q += r >= d ? 1 : (r < 0 ? -1 : 0);
+    return q;
+  };
   auto tile_at = [&](int tile, int& mb, int& nb) {
     const int per_group = p.group_m * p.num_n;
-    const int gid = tile / per_group;
+    const int gid = quotient(tile, per_group, p.inv_per_group);
     const int first_m = gid * p.group_m;
     const int gm = min(p.num_m - first_m, p.group_m);
     const int r = tile - gid * per_group;
-    mb = first_m + r % gm;
-    nb = r / gm;
+    nb = quotient(r, gm, gm == p.group_m ? p.inv_group_m : __frcp_rn(static_cast<float>(gm)));
+    mb = first_m + r - nb * gm;
   };
 
   if (warp >= kF8Warps) {

@@ -340,6 +340,8 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
                                   : static_cast<int>(N_out / 128);
   p.num_tiles = p.num_m * p.num_n;
   p.group_m = kGemmGroupRows < p.num_m ? kGemmGroupRows : p.num_m;
+  p.inv_per_group = 1.0f / (static_cast<float>(p.group_m) * static_cast<float>(p.num_n));
+  p.inv_group_m = 1.0f / static_cast<float>(p.group_m);
   p.b_row_up = (EPI == h3q::kF8BF16) ? 0 : static_cast<int>(N_out);
   p.last_nb = static_cast<int>((b_rows + 127) / 128) - 1;
   p.sx = sx;
