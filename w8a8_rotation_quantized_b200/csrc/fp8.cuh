@@ -648,22 +648,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && row0 < p.M) tma_store_2d(&tmOut, out_tile, n0, row0);
+        if (lane == 0 && row0 < p.M) {
+          tma_store_2d(&tmOut, out_tile, n0, row0);
+          bulk_commit();
+        }
       } else {
+        const int n0 = nb * kBN + 32 * part;  // and n0 + 128
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
-          const int n0 = nb * kBN + 128 * pass + 32 * part;
-          if (n0 < p.N) {
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-              if (p.bias != nullptr && n0 + 8 * g < p.N) f8_bias8(&acc[pass][8 * g], p.bias + n0 + 8 * g);
-              *reinterpret_cast<uint4*>(out_tile + pass * kF8OutTile + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) =
-                  f8_pack8(&acc[pass][8 * g]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0 && row0 < p.M) tma_store_2d(&tmOut, out_tile + pass * kF8OutTile, n0, row0);
+          for (int g = 0; g < 4; ++g) {
+            const int n = n0 + 128 * pass + 8 * g;
+            if (p.bias != nullptr && n < p.N) f8_bias8(&acc[pass][8 * g], p.bias + n);
+            *reinterpret_cast<uint4*>(out_tile + pass * kF8OutTile + lane * 64 + ((g ^ (lane >> 1)) & 3) * 16) =
+                f8_pack8(&acc[pass][8 * g]);
           }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && row0 < p.M) {
+          if (n0 < p.N) tma_store_2d(&tmOut, out_tile, n0, row0);
+          if (n0 + 128 < p.N) tma_store_2d(&tmOut, out_tile + kF8OutTile, n0 + 128, row0);
+          bulk_commit();
         }
       }
     }

@@ -276,15 +276,17 @@ __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* m
 }
 
 // 2D tiled store of one box from shared memory (written by ordinary stores and made
-// visible by fence_proxy_async_smem), one bulk group of the issuing thread; what lies
-// past the tensor's edges is left out.
+// visible by fence_proxy_async_smem), part of the issuing thread's open bulk group; what
+// lies past the tensor's edges is left out.
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* smem_src, int32_t x, int32_t y) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%2, %3}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(map)),
                "r"(smem_u32(smem_src)), "r"(x), "r"(y)
                : "memory");
-  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
+
+// Closes the thread's open bulk group.
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 
 // Waits until at most N of this thread's latest bulk groups have yet to read their
 // shared memory.
