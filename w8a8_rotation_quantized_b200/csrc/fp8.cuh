@@ -288,6 +288,7 @@ __device__ __forceinline__ void f8_bias32(float* acc, const __nv_bfloat16* bias)
 
 enum Fp8Epi : int { kF8BF16 = 0, kF8SwiGLU = 1, kF8SwiGLUQuant = 2 };
 
+constexpr int64_t kF8MaxTiles = int64_t(1) << 23;  // output tiles of a call (the host refuses more)
 constexpr int kF8Stages = 4;
 constexpr int kF8Warps = 16;                     // promotion warps
 constexpr int kF8Threads = 32 * kF8Warps + 128;  // then operand and scale producers, two MMA issuers
@@ -321,8 +322,9 @@ struct Fp8Params {
   uint64_t wait_limit_ns;
 };
 
-// acc += part * f, 32 columns, two multiply-adds an instruction: the same rate as
-// single ones, and half the issue slots, which the control warps need.
+// acc += part * f, 32 columns, two multiply-adds an instruction: the same rate as single
+// ones (664 against 712 cycles a K block) at half the issue slots, which the control warps
+// need.
 __device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&r)[32], float f) {
 #pragma unroll
   for (int i = 0; i < 32; i += 2) {
@@ -333,14 +335,31 @@ __device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&r)
   }
 }
 
-// CTA pairs, 256 x 256 output tiles, TMA ring and cta_group::2 MMAs as in the int8
-// GEMM. The tensor cores sum one K block of 128 at a time (four MMAs) into one of
-// two 256-column buffers of tensor memory; the promotion warps read each block's
-// partial sums, multiply them by the block's scales and add them to fp32
-// accumulators in registers (128 columns of one row per thread), while the tensor
-// cores fill the other buffer. Per SM and K block the MMAs take 512 cycles, reading
-// 128 KB of partial sums 256, and the 128 x 256 multiply-adds 256 of the fp32
-// pipe: the tensor cores stay the bound.
+// Large products. CTA pairs, 256 x 256 output tiles, TMA ring and cta_group::2 MMAs as in
+// the int8 GEMM. The tensor cores sum one K block of 128 at a time (four MMAs) into one of
+// two 256-column buffers of tensor memory; sixteen promotion warps read each block's
+// partial sums, multiply them by the block's scales and add them to fp32 accumulators in
+// registers (64 columns of one row per thread) while the tensor cores fill the other
+// buffer. Roles:
+//   warps 0-15   promotion and output;
+//   warp 16      operand tiles by TMA (both CTAs), warp 17 the block scales (cp.async, up
+//                to sixteen blocks ahead), each a warp of its own, since the promotion
+//                warps take the issue slots;
+//   warps 18-19  MMA issue (leader CTA), one per buffer, so that each has two K blocks'
+//                time for one.
+// What bounds it: per SM and K block the MMAs take 512 cycles, reading the 128 KB of
+// partial sums 256 and their multiply-adds 256 of the fp32 pipe, in parallel. Measured 640
+// to 665 cycles a K block and some 2700 an output tile between blocks; the same kernel
+// promoting once a tile (other results, for the comparison) takes 520. At random data the
+// board's power limit sets in: 4096 x 5376 x 16128 takes 226 us at the full 1.84 GHz (zero
+// operands) and 280 at the 1.5 GHz that the limit leaves, 16384 x 14336 x 5376 1.04 ms at
+// 1.36 GHz. What counted on the way (16384 x 14336 x 5376, 3.0 ms at first): arrivals at
+// the partner CTA without a cluster-scope release (-40%); control roles run by converged
+// warps, their descriptors in uniform registers; scales fetched ahead instead of one block
+// before (-15%); no register spills (addresses of shared memory as constants); the next
+// block's scales and completion test fetched behind the release of this one (-15%). Halves
+// of a block as MMAs of 128 columns ran slower (the A tile is read twice for the same
+// work), and so did promotion by eight warps of 128 columns each.
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -405,8 +424,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   grid_dependency_wait();
 
   // Tiles run down groups of group_m row blocks, as in the int8 GEMM. The quotients come
-  // from a product with the reciprocal and one correction, exact below 2^23 tiles (more
-  // would be a terabyte of output): an integer division here costs more than a K block.
+  // from a product with the reciprocal and one correction, exact up to kF8MaxTiles: an
+  // integer division here costs as much as half a K block.
   auto quotient = [](int n, int d, float inv) {
     int q = static_cast<int>(__fmul_rn(static_cast<float>(n), inv));
     const int r = n - q * d;

@@ -732,7 +732,7 @@ static h3q_status check_fp8_args(const uint8_t* xq, const float* sx, int64_t M, 
                                  const float* sw, int64_t N, const void* bias) {
   if (M < 0 || !valid_fp8_k(K) || N <= 0 || N % 8 != 0) return H3Q_ERR_INVALID_ARG;
   if (M > INT32_MAX - 256 || N > INT32_MAX - 512 || K > INT32_MAX - 256) return H3Q_ERR_UNSUPPORTED;
-  if (((M + 255) / 256) * ((N + 127) / 128) > INT32_MAX / 2) return H3Q_ERR_UNSUPPORTED;
+  if (((M + 255) / 256) * ((N + 255) / 256) > h3q::kF8MaxTiles) return H3Q_ERR_UNSUPPORTED;
   if (M == 0) return H3Q_OK;
   if (!xq || !sx || !wq || !sw || !aligned16(xq) || !aligned16(sx) || !aligned16(wq) || !aligned16(sw) ||
       (bias && !aligned16(bias)))
