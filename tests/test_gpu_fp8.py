@@ -357,6 +357,104 @@ def test_ffn_captured_and_replayed(h3q, cuda_device, M):
     assert h3q.h3q_get_device_status() == h3q.H3Q_OK
 
 
+def test_buffers_reused_without_a_pause(h3q, cuda_device):
+    """Each call may start while the one before it ends: operands that are overwritten by the next
+    step of a chain, call after call, still give what each step gives by itself."""
+    M, K, N = 40, 1360, 1280
+    wq, sw = _prepare(h3q, torch.randn(N, K, generator=torch.Generator().manual_seed(1)).to(cuda_device) * 0.02)
+    xs = [_input(M, K, 10 + i, cuda_device) for i in range(30)]
+    want = []
+    for x in xs:
+        y = torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device)
+        h3q.h3q_linear_fp8(*_quantize(h3q, x), wq, sw, y)
+        torch.cuda.synchronize()
+        want.append(y)
+    xq, sx = _quantize(h3q, xs[0])
+    y = torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device)
+    got = []
+    for x in xs:
+        h3q.h3q_fp8_quantize(x, xq, sx)
+        h3q.h3q_linear_fp8(xq, sx, wq, sw, y)
+        got.append(y.clone())
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_graphs_replayed_at_once(h3q, cuda_device):
+    streams, graphs, sets = [torch.cuda.Stream() for _ in range(2)], [], []
+    for M, st in zip((6, 400), streams):
+        ops = _operands(h3q, M, 2064, 1024, M, cuda_device, False)[:4]
+        got = [torch.empty(M, 512, dtype=E4, device=cuda_device), torch.empty(4, M, device=cuda_device)]
+        want = [torch.empty_like(t) for t in got]
+        h3q.h3q_linear_fp8_swiglu_quant(*ops, *want)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            for _ in range(4):
+                h3q.h3q_linear_fp8_swiglu_quant(*ops, *got)
+        graphs.append(graph)
+        sets.append((ops, got, want))
+    for _ in range(3):
+        for graph, st in zip(graphs, streams):
+            with torch.cuda.stream(st):
+                graph.replay()
+    torch.cuda.synchronize()
+    for _, got, want in sets:
+        assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+
+
+def _some(n):
+    """Rows at both ends, and at and past element 2^31 of rows of 14336."""
+    return torch.cat([torch.arange(0, 3), torch.arange(149795, 149799), torch.arange(n - 3, n)])
+
+
+@pytest.mark.parametrize("weight", [False, True])
+def test_quantizers_past_32_bits(h3q, cuda_device, weight):
+    M, K = 150001, 14336
+    x = torch.zeros(M, K, dtype=torch.bfloat16, device=cuda_device)
+    rows = _some(M)
+    x[rows.to(cuda_device)] = _input(len(rows), K, 5, cuda_device)
+    codes, s = (_prepare if weight else _quantize)(h3q, x)
+    if weight:  # whole bands of 128 rows
+        for f in (rows // 128 * 128).unique().tolist():
+            c, sc = _quantize_ref(x[f : f + 128].float().cpu().numpy(), 128)
+            assert np.array_equal(s[f // 128].cpu().numpy(), sc[0])
+            assert np.array_equal(codes[f : f + 128].float().cpu().numpy(), c)
+    else:
+        c, sc = _quantize_ref(x[rows.to(cuda_device)].float().cpu().numpy(), 1)
+        assert np.array_equal(s[:, rows.to(cuda_device)].cpu().numpy(), sc.T)
+        assert np.array_equal(codes[rows.to(cuda_device)].float().cpu().numpy(), c)
+
+
+@pytest.mark.parametrize("M,N", [(150001, 14344), (40, 53700008)])
+def test_linear_past_32_bits(h3q, cuda_device, M, N):
+    K = 16
+    w = torch.randn(99991, K, generator=torch.Generator().manual_seed(4)).to(cuda_device)
+    wq, sw = _prepare(h3q, w.repeat(-(-N // 99991), 1)[:N])
+    xq, sx = _quantize(h3q, _input(M, K, 3, cuda_device))
+    y = torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device)
+    h3q.h3q_linear_fp8(xq, sx, wq, sw, y)
+    rows = (_some(M) if M > 1000 else torch.arange(36, 40)).to(cuda_device)
+    for lo in (0, N // 2 // 128 * 128, (N - 4000) // 128 * 128):
+        hi = min(lo + 4096, N)
+        v, mag = _product_ref(xq[rows], sx[:, rows].contiguous(), wq[lo:hi], sw[lo // 128 : -(-hi // 128)], None)
+        e = _err(v, mag, K)
+        _close(y[rows, lo:hi], v, e + 2.0 ** -8 * (v.abs() + e))
+
+
+def test_swiglu_quant_past_32_bits(h3q, cuda_device):
+    M, K, F = 150001, 16, 14336
+    xq, sx, wq, sw, _ = _operands(h3q, M, K, 2 * F, 3, cuda_device, False)
+    hq, sh = torch.empty(M, F, dtype=E4, device=cuda_device), torch.empty(F // 128, M, device=cuda_device)
+    h3q.h3q_linear_fp8_swiglu_quant(xq, sx, wq, sw, hq, sh)
+    rows = _some(M).to(cuda_device)
+    v, mag = _product_ref(xq[rows], sx[:, rows].contiguous(), wq, sw, None)
+    h, e = _swiglu_ref(v, _err(v, mag, K))
+    s = sh[:, rows].T.double().repeat_interleave(128, dim=1)
+    half_step = torch.maximum(2.0 ** -4 * (h.abs() + e), 2.0 ** -10 * s)
+    _close(hq[rows].double() * s, h, e + half_step * (1 + 2.0 ** -20) + 2.0 ** -126)
+
+
 def test_binding_refuses_wrong_shapes(h3q, cuda_device):
     xq, sx, wq, sw, bias = _operands(h3q, 5, 272, 264, 1, cuda_device, True)
     y = torch.empty(5, 264, dtype=torch.bfloat16, device=cuda_device)

@@ -261,8 +261,9 @@ __device__ __forceinline__ void tmem_ld_wait32(uint32_t (&r)[32]) {
 // enters as a factor 1 + lo ln 2, and the reciprocal takes one Newton step. What is left is
 // the error of 2^x itself (two units of the last place), as in an fp32 evaluation. The
 // error of a quantized output, which is that of codes on the other side of a border, halves
-// (1.1e-4 to 5e-5 of its norm at 16384 x 5376 -> 14336) for 1% of that call's time. Below g = -87.3 the reciprocal leaves the normal range and the
-// result is -0; silu is above -2^-119 there.
+// (1.1e-4 to 5e-5 of its norm at 16384 x 5376 -> 14336) for 1% of that call's time. Below
+// g = -87.3 the reciprocal leaves the normal range and the result is -0; silu is above
+// -2^-119 there.
 __device__ __forceinline__ float silu_approx(float g) {
   const float t = fminf(__fmul_rn(g, -1.44269504f), 126.0f);  // 2^t stays finite
   const float lo = __fmaf_rn(g, -1.92596299e-8f, __fmaf_rn(g, -1.44269504f, -t));
@@ -483,8 +484,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
           }
         }
       }
-      if (!ok && rank == 0) {
-        // drain the copies that may still be in flight (bounded, ignores abort)
+      if (rank == 0) {
+        // the last copies, which nobody else waits for where a role gave up (bounded, ignores abort)
         for (int m = n - 1; m >= 0 && m >= n - kF8Stages; --m)
           mbar_wait_bounded(&full[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr);
       }
@@ -730,7 +731,9 @@ struct Fp8Small {
   static constexpr int kCols = R * TM;                       // tensor-memory columns of one K block
   static constexpr int kHalf = kCols / 2;                    // columns of a promotion thread
   static constexpr int kBufs = kCols > 128 ? 2 : 4;
-  // tensor memory is allocated by powers of two
+  // Tensor memory is allocated by powers of two. CTAs of any variants that share an SM (by
+  // registers) need 512 columns together at most, so no allocation waits for a CTA whose
+  // cluster waits for this one.
   static constexpr int kTmem = kCols * kBufs <= 64 ? 64 : kCols * kBufs <= 128 ? 128 : kCols * kBufs <= 256 ? 256 : 512;
   static constexpr int kPartials = R * TM * 128 * 4;
   static_assert(kPartials <= 3 * kStage, "the partial sums fit in the operand ring");
@@ -895,10 +898,9 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
         phase ^= 1u;
       }
     }
-    // past a wait that ran out: the copies still in flight (bounded, ignores abort)
-    if (i < nkb)
-      for (int m = i - 1; m >= 0 && m >= i - S; --m)
-        mbar_wait_bounded(&full[m % S], static_cast<uint32_t>((m / S) & 1), limit, nullptr);
+    // the last copies, which nobody else waits for where a role gave up (bounded, ignores abort)
+    for (int m = i - 1; m >= 0 && m >= i - S; --m)
+      mbar_wait_bounded(&full[m % S], static_cast<uint32_t>((m / S) & 1), limit, nullptr);
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc = idesc_fp8(128, TM);

@@ -223,7 +223,9 @@ h3q_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threa
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = cluster > 0 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess ? H3Q_OK : H3Q_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess) return H3Q_OK;
+  cudaGetLastError();  // reported here, not by the caller's next check
+  return H3Q_ERR_CUDA;
 }
 
 // How the kernel for few tokens would run: CTAs per tile along K, and an estimate of its
