@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const T* __restrict__
   const int64_t m0 = int64_t(rb) * kF8QuantRows;
   const int64_t first = (m0 + 4 * warp) * K + col;
   const int rows = col < K ? static_cast<int>(min(int64_t(4), M - m0 - 4 * warp)) : 0;  // of this warp, may be negative
+  grid_dependents_start();
   grid_dependency_wait();
   Fp8Chunk<T> v[4];
 #pragma unroll
@@ -429,6 +430,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
   cluster_sync();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  grid_dependents_start();
   grid_dependency_wait();
 
   // Tiles run down groups of group_m row blocks, as in the int8 GEMM. The quotients come
@@ -884,6 +886,7 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xFFFFFFFFu, *tmem_slot, 0);
+  grid_dependents_start();
   grid_dependency_wait();
 
   if (warp == 8) {

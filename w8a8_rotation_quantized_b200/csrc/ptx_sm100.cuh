@@ -155,6 +155,12 @@ __device__ __forceinline__ bool mbar_wait_bounded_warp(uint64_t* bar, uint32_t p
 // and writes no global memory before this.
 __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lets a programmatic dependent of this kernel start once every block of it has come here
+// (or ended): the dependent's own grid_dependency_wait still waits for this kernel's end.
+// A block calls it with all that it has to allocate in hand, so that the dependent's
+// blocks can take none of it.
+__device__ __forceinline__ void grid_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;

@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
   const int steps_q = (p.Hq + kHeads - 1) / kHeads, steps_k = (p.Hk + kHeads - 1) / kHeads;
   const int per = (steps_q + steps_k + gridDim.y - 1) / gridDim.y;
   const int begin = blockIdx.y * per, end = min(begin + per, steps_q + steps_k);
+  grid_dependents_start();
   grid_dependency_wait();
   const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
   for (int64_t t = int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5); t < p.S; t += warps) {
