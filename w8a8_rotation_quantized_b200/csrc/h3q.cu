@@ -259,8 +259,8 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
   // cluster sits in one GPC, so the larger it is the more SMs stay over: what still fitted
   // was seven eighths of the SMs for three and four, two thirds for six and eight (four
   // thirds at two an SM); past it a launch takes a second round (24 clusters of six: 30 us
-  // instead of 18). One token, K 5376, in a graph: N 5376 split six ways 10.4 us, four
-  // 11.0, not 19.1; N 16128 two 20.3, not 21.4; SwiGLU to 14336 not 28.7, two 29.3.
+  // instead of 18). One token, K 5376, in a graph: N 5376 split six ways 9.3 us, four
+  // 9.0, not 18.1; N 16128 two 17.4, not 19.2; SwiGLU to 14336 not 27.0, two 27.6.
   const bool fits_two = R * TM <= 64;
   Fp8SmallPlan pl{1, false, 0.0};
   for (const int s : {2, 3, 4, 6, 8}) {
@@ -271,7 +271,7 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
   }
   // Half of an SM's shared memory for the ring where two CTAs fit, so that the next
   // launch's find room beside this one's; all of it for the long streams of an unsplit
-  // gate/up product (28.7 against 30.4 us).
+  // gate/up product (27.0 against 29.2 us).
   pl.two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
   const int64_t rounds = (tiles * pl.splits + sms - 1) / sms;
   pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs +
@@ -287,7 +287,8 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
   using Cfg = h3q::Fp8Small<R, TM>;
   CUtensorMap tw, tx;
-  if (!make_tmap_i8(&tw, w, w_rows, K) || !make_tmap_i8(&tx, x, M, K, TM)) return H3Q_ERR_CUDA;
+  const int x_rows = static_cast<int>(std::min<int64_t>(M, TM));
+  if (!make_tmap_i8(&tw, w, w_rows, K) || !make_tmap_i8(&tx, x, M, K, x_rows)) return H3Q_ERR_CUDA;
   const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_small_kernel<EPI, TM>);
   if (ensure_smem_attr(kernel, 232448) != cudaSuccess) return H3Q_ERR_CUDA;
   h3q::Fp8SmallParams p{};
@@ -307,6 +308,7 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   const int64_t tiles = int64_t(p.num_m) * p.num_n;
   const int splits = plan.splits;
   p.splits = splits;
+  p.x_rows = x_rows;
   const int room = (plan.two ? 113 * 1024 : 226 * 1024) - Cfg::kFixed;
   p.stages = std::min(std::min(room / Cfg::kStage, h3q::kF8sMaxStages), std::max(3, (p.KB + splits - 1) / splits));
   const size_t smem = size_t(p.stages) * Cfg::kStage + Cfg::kFixed;
