@@ -299,6 +299,9 @@ enum Fp8Epi : int { kF8BF16 = 0, kF8SwiGLU = 1, kF8SwiGLUQuant = 2 };
 
 constexpr int64_t kF8MaxTiles = int64_t(1) << 23;  // output tiles of a call (the host refuses more)
 constexpr int kF8Stages = 4;
+// The two issuers take the K blocks in turn and each keeps its own stages: with an odd ring a
+// stage would change hands, and the parity that its next owner waits for holds one round early.
+static_assert(kF8Stages % 2 == 0, "a stage belongs to one issuer");
 constexpr int kF8Warps = 16;                     // promotion warps
 constexpr int kF8Threads = 32 * kF8Warps + 128;  // then operand and scale producers, two MMA issuers
 constexpr int kF8Producer = kF8Warps, kF8Issuer = kF8Warps + 2;
