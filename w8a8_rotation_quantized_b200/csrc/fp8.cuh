@@ -726,9 +726,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 // K axis, the tokens that fall to it and writes them out (a warp per token, four
 // columns a lane), so the result does not depend on timing and nothing is kept in
 // global memory.
-// Token rows that do not exist are not loaded: the TMA would fill them with zeros, but is
-// slow at it (one token, 5376 x 28672: 34.3 us with 15 such rows a load, 28.4 without). What
-// their place in shared memory holds reaches only columns that are not written.
+// The tokens are shared out evenly over the tiles, and rows that do not exist are not
+// loaded: the TMA would fill them with zeros, but is slow at it (one token, 5376 x 28672:
+// 34.3 us with 15 such rows a load, 28.4 without). What their place in shared memory holds
+// reaches only columns that are not written.
 constexpr int kF8sMaxStages = 12;
 constexpr int kF8sThreads = 384;  // eight promotion warps, operands, MMA, scales, one idle until the output
 constexpr int kF8sScaleRing = 16;
@@ -753,7 +754,7 @@ struct Fp8SmallParams {
   int M, N, KB;
   int num_m, num_n;    // token tiles, row tiles
   int stages, splits;  // ring depth; CTAs per cluster
-  int x_rows;          // token rows of a load: TM, or M where that is less
+  int x_rows;          // token rows of a tile: ceil(M / num_m), at most TM
   int up_row;          // SwiGLU: first up row of the weight (= F)
   int swiglu_rows;     // F / 128
   const float *sx, *sw;
@@ -861,7 +862,7 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
     mbar_arrive_expect_tx(&full[stage], R * 128 * 128 + p.x_rows * 128);
     tma_load_2d(dst, &tmW, &full[stage], k, nt * 128, pol);
     if (R == 2) tma_load_2d(dst + 128 * 128, &tmW, &full[stage], k, p.up_row + nt * 128, pol);
-    tma_load_2d(dst + R * 128 * 128, &tmX, &full[stage], k, mt * TM, pol);
+    tma_load_2d(dst + R * 128 * 128, &tmX, &full[stage], k, mt * p.x_rows, pol);
   };
   if (warp == 8) {
     if (one) {
@@ -955,8 +956,8 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
 #pragma unroll
       for (int j = 0; j < (TM + 31) / 32; ++j) {
         const int m = 32 * j + lane;
-        const bool in = mt * TM + m < p.M;
-        if (m < TM) cp_async4(dst + m * 4, in ? p.sx + kb * p.M + mt * TM + m : p.sx, in);
+        const bool in = m < p.x_rows && mt * p.x_rows + m < p.M;
+        if (m < TM) cp_async4(dst + m * 4, in ? p.sx + kb * p.M + mt * p.x_rows + m : p.sx, in);
       }
       if (lane < R) cp_async4(dst + TM * 4 + lane * 4, p.sw + int64_t(nt + lane * p.swiglu_rows) * p.KB + kb, true);
       if ((i & 3) == 3 || i == nkb - 1) cp_async_arrive(&sfull[(i >> 2) & 3]);
@@ -1024,10 +1025,10 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
   tc_fence_after();
 
   // ------------------------------------------------------------ sums over the cluster and output
-  const int per = (TM + p.splits - 1) / p.splits;
+  const int per = (p.x_rows + p.splits - 1) / p.splits;
   const int n = nt * 128 + 4 * lane;  // this lane's four columns (SwiGLU: of h)
-  for (int m = rank * per + warp; m < min(rank * per + per, TM); m += kF8sThreads / 32) {
-    const int row = mt * TM + m;
+  for (int m = rank * per + warp; m < min(rank * per + per, p.x_rows); m += kF8sThreads / 32) {
+    const int row = mt * p.x_rows + m;
     if (row >= p.M) break;
     float4 v[R];
 #pragma unroll

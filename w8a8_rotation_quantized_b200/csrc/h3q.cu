@@ -287,7 +287,8 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
   using Cfg = h3q::Fp8Small<R, TM>;
   CUtensorMap tw, tx;
-  const int x_rows = static_cast<int>(std::min<int64_t>(M, TM));
+  const int64_t num_m = (M + TM - 1) / TM;
+  const int x_rows = static_cast<int>((M + num_m - 1) / num_m);
   if (!make_tmap_i8(&tw, w, w_rows, K) || !make_tmap_i8(&tx, x, M, K, x_rows)) return H3Q_ERR_CUDA;
   const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_small_kernel<EPI, TM>);
   if (ensure_smem_attr(kernel, 232448) != cudaSuccess) return H3Q_ERR_CUDA;
@@ -295,7 +296,7 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N_out);
   p.KB = static_cast<int>((K + 127) / 128);
-  p.num_m = static_cast<int>((M + TM - 1) / TM);
+  p.num_m = static_cast<int>(num_m);
   p.num_n = static_cast<int>((N_out + 127) / 128);
   p.up_row = R == 2 ? static_cast<int>(N_out) : 0;
   p.swiglu_rows = p.up_row / 128;
