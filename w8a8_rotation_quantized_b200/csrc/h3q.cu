@@ -236,22 +236,21 @@ struct Fp8SmallPlan {
   double us;
 };
 
-// Which fp8 product runs is decided by estimates from measured times of one K block of
-// one tile on one SM (pair), times the rounds over the SMs. Few tokens: 0.42 us up to 64
-// tokens a tile (two weight tiles a K block, SwiGLU: 0.60 from 48 tokens), 0.45 at 96
-// (SwiGLU 0.70), 0.48 at 128 (SwiGLU 1.07); 4 us for launch and ends (5.5 with 96 or more
-// rows of sums to hand over), 1 more with a split K axis, 2.5 more with large clusters
-// that share their SMs. The large kernel: 0.45 us for its 256 x 256 tile of two SMs, and
-// 5 us. Measured on both sides of the border, for example (us, few tokens against large):
-// 64 x 5376 x 5376 14.2, 24.2; 512 x 14336 x 1024 19.6, 56.8; 256 x 5376 x 16128 48.1,
-// 28.6; SwiGLU 128 x 1360 -> 2176 9.8, 11.5; 384 x 1360 -> 2176 14.5, 12.0.
-constexpr double kF8LargeStepUs = 0.45, kF8LargeFixedUs = 5.0;
+// Which fp8 product runs is decided by estimates of their times, fitted to measured ones
+// (330 random shapes of 49 to 1500 tokens, K to 14336, each by every kernel, in a graph; the
+// choice costs 1% over the best of them on the mean): the rounds over the SMs times the K
+// blocks of a tile times a step, the ends of the call, and what every further round adds.
+// The large kernel's tile is 256 x 256 on two SMs. Measured on both sides of the border, for
+// example (us, few tokens against large): 169 x 5216 x 3680 14.8, 20.9; 157 x 10032 x 584
+// 10.5, 36.5; 161 x 2672 x 7024 16.7, 14.6; 413 x 4240 x 12208 64.3, 36.0; SwiGLU 82 x 6896
+// -> 1024 11.7, 25.4; 145 x 288 -> 256 6.6, 5.8; 295 x 4976 -> 4352 38.3, 22.6.
+constexpr double kF8LargeStepUs = 0.39, kF8LargeFixedUs = 5.0, kF8LargeRoundUs = 2.1;
 
 template <int R, int TM>
 Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
-  constexpr double kStepUs = TM == 128  ? (R == 2 ? 1.07 : 0.48)
-                             : TM == 96 ? (R == 2 ? 0.70 : 0.45)
-                                        : (R == 2 && TM >= 48 ? 0.60 : 0.42);
+  constexpr double kStepUs = R == 1 ? (TM == 128 ? 0.525 : TM == 96 ? 0.475 : 0.40) : (TM == 128 ? 0.935 : TM == 96 ? 0.66 : 0.575);
+  constexpr double kFixedUs = R == 1 ? (TM == 128 ? 4.9 : 4.3) : (TM == 128 ? 7.5 : TM == 96 ? 6.2 : 5.2);
+  constexpr double kRoundUs = R == 1 ? (TM == 128 ? 5.5 : TM == 96 ? 4.9 : 2.0) : (TM == 128 ? 8.7 : TM == 96 ? 7.1 : 6.2);
   const int64_t tiles = ((M + TM - 1) / TM) * ((N_out + 127) / 128);
   // Split the K axis as far as the CTAs find room and two K blocks are left to each (four
   // with eight CTAs): up to seven quarters of the SMs where two CTAs fit an SM
@@ -273,10 +272,11 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
   // launch's find room beside this one's; all of it for the long streams of an unsplit
   // gate/up product (27.0 against 29.2 us).
   pl.two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
-  const int64_t rounds = (tiles * pl.splits + sms - 1) / sms;
-  pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs +
-          (R * TM >= 96 ? 5.5 : 4.0) + (pl.splits > 1 ? 1.0 : 0.0) +
-          (TM == 64 && pl.splits >= 6 ? 2.5 : 0.0);
+  const int64_t ctas = tiles * pl.splits, rounds = (ctas + sms - 1) / sms;
+  pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs + kFixedUs + double(rounds - 1) * kRoundUs +
+          (pl.splits > 1 ? 0.25 : 0.0) + (pl.splits >= 6 ? 0.5 : 0.0);
+  // with nearly as many CTAs as SMs and room for two, some SMs get two while others idle
+  if (fits_two && ctas > int64_t(sms) * 7 / 8 && ctas <= sms) pl.us *= 1.3;
   return pl;
 }
 
@@ -380,7 +380,8 @@ h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t
     return launch_gemm_fp8_small<EPI, 48>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
                                           plan_gemm_fp8_small<R, 48>(M, N_out, KB, sms), stream);
   const int64_t large_tiles = ((M + 255) / 256) * (R == 1 ? (N_out + 255) / 256 : N_out / 128);
-  const double large_us = double((large_tiles + sms / 2 - 1) / (sms / 2)) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs;
+  const int64_t large_rounds = (large_tiles + sms / 2 - 1) / (sms / 2);
+  const double large_us = double(large_rounds) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs + double(large_rounds - 1) * kF8LargeRoundUs;
   const Fp8SmallPlan p64 = plan_gemm_fp8_small<R, 64>(M, N_out, KB, sms);
   const Fp8SmallPlan p96 = plan_gemm_fp8_small<R, 96>(M, N_out, KB, sms);
   const Fp8SmallPlan p128 = plan_gemm_fp8_small<R, 128>(M, N_out, KB, sms);
