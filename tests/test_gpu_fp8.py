@@ -403,6 +403,33 @@ def test_two_graphs_replayed_at_once(h3q, cuda_device):
         assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
 
 
+def test_large_products_back_to_back(h3q, cuda_device):
+    """Launch upon launch of CTA pairs, of one K block and of numbers that leave every place of the
+    operand ring last, so that blocks start where others have just left: each product as by itself,
+    and no wait ran out."""
+    M, N = 1500, 2056
+    sets = [_operands(h3q, M, K, N, K, cuda_device, False)[:4] for K in (16, 144, 272, 400, 512, 656, 1040)]
+    want, got = ([torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device) for _ in sets] for _ in range(2))
+    for s, t in zip(sets, want):
+        h3q.h3q_linear_fp8(*s, t)
+        torch.cuda.synchronize()
+        v, mag = _product_ref(*s, None)
+        e = _err(v, mag, s[0].shape[1])
+        _close(t, v, e + 2.0 ** -8 * (v.abs() + e))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(20):
+            for s, t in zip(sets, got):
+                h3q.h3q_linear_fp8(*s, t)
+    for _ in range(3):
+        for t in got:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+
+
 def _some(n):
     """Rows at both ends, and at and past element 2^31 of rows of 14336."""
     return torch.cat([torch.arange(0, 3), torch.arange(149795, 149799), torch.arange(n - 3, n)])

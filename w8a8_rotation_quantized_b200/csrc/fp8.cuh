@@ -494,6 +494,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         for (int m = n - 1; m >= 0 && m >= n - kF8Stages; --m)
           mbar_wait_bounded(&full[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr);
       }
+      // The issuers' last arrivals at this CTA's `empty`. They come from the leader, and neither
+      // `tfull` nor `drain` says that they have landed here: a CTA that left earlier would have
+      // them arrive in shared memory that is the next one's. One wait that runs out is enough:
+      // what it waited for does not come any more.
+      for (int m = n - 1; m >= 0 && m >= n - kF8Stages; --m)
+        if (!mbar_wait_bounded(&empty[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr)) break;
     } else if (warp == kF8Producer + 1) {
       // ------------------------------------------------------------ scales (both CTAs)
       // Up to sixteen K blocks ahead: each lane copies four rows'
