@@ -283,6 +283,14 @@ h3q_status h3q_linear_fp8_swiglu_quant(const uint8_t* xq, const float* sx, int64
                                        cudaStream_t stream);
 
 /*
+ * Test hook, host only: how the fp8 products run this size on a GPU of `sms` SMs.
+ * plan[5]: tokens of a tile of the kernel for few tokens (0: the large kernel); CTAs per
+ * tile along K; operand stages; bytes of shared memory and columns of tensor memory of a
+ * CTA. epilogue H3Q_EPI_SWIGLU stands for both SwiGLU forms.
+ */
+h3q_status h3q_test_fp8_plan(int64_t M, int64_t K, int64_t N, int epilogue, int sms, int32_t* plan);
+
+/*
  * RMS norm of every query and key head and the rotation of positions, in one pass
  * (the step between the QKV projection and the attention; h3-rs README and the
  * vllm-omni issue name it fused).

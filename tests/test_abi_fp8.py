@@ -1,6 +1,8 @@
 """Host-side checks of the fp8 linear calls and the query/key norm: each call below fails
 them (or has nothing to do), so nothing is launched and no pointer is followed."""
 import ctypes
+import math
+import random
 
 import pytest
 
@@ -115,3 +117,38 @@ def test_signatures_match_the_header():
         text = open(h3q.HEADER).read().split(name + "(", 1)[1].split(");", 1)[0]
         assert text.count(",") + 1 == n == len(getattr(h3q.lib, name).argtypes)
         assert isinstance(getattr(h3q.lib, name), ctypes._CFuncPtr)
+
+
+def test_plan_rejects():
+    plan = (ctypes.c_int32 * 5)()
+    ok = [4, 512, 512, 0, 148, plan]
+    for i, bad in [(0, 0), (1, 8), (1, 520), (2, 0), (2, 12), (3, 2), (4, 1), (5, None)]:
+        args = list(ok)
+        args[i] = bad
+        assert h3q.lib.h3q_test_fp8_plan(*args) == INV, (i, bad)
+    assert h3q.lib.h3q_test_fp8_plan(4, 512, 384, h3q.H3Q_EPI_SWIGLU, 148, plan) == INV
+    assert h3q.lib.h3q_test_fp8_plan(*ok) == OK
+
+
+def _sizes(epilogue, n=30000):
+    """M, K, N spread over what the products take, small and large."""
+    rng = random.Random(epilogue)
+    step = 256 if epilogue else 8
+
+    def spread(lo, hi):
+        return int(math.exp(rng.uniform(math.log(lo), math.log(hi))))
+    for _ in range(n):
+        yield spread(1, 4000), 16 * spread(1, 900), step * spread(1, 38000 // step)
+
+
+@pytest.mark.parametrize("epilogue", [h3q.H3Q_EPI_NONE, h3q.H3Q_EPI_SWIGLU])
+def test_every_variant_of_the_products_is_tested(epilogue):
+    """The GPU tests' lists hold a size for each kernel and split that the rule on sizes picks."""
+    pytest.importorskip("torch")
+    from test_gpu_fp8 import LINEAR_VARIANTS, SWIGLU_VARIANTS
+    listed = SWIGLU_VARIANTS if epilogue else LINEAR_VARIANTS
+    for M, K, N, tile, splits in listed:
+        assert h3q.h3q_test_fp8_plan(M, K, 2 * N if epilogue else N, epilogue)[:2] == (tile, splits), (M, K, N)
+    picked = {h3q.h3q_test_fp8_plan(M, K, N, epilogue)[:2] for M, K, N in _sizes(epilogue)}
+    assert picked <= {v[3:] for v in listed}
+    assert {v[3] for v in listed} == {0, 16, 32, 48, 64, 96, 128}

@@ -240,6 +240,39 @@ def test_swiglu_over_split_and_many_tiles(h3q, cuda_device, M, K, F):
     test_swiglu_within_bound(h3q, cuda_device, M, K, F, M % 2 == 0)
 
 
+# Every kernel that the rule on sizes picks (M, K, columns of the output, tokens of a tile or 0 for
+# the large kernel, CTAs along K), at odd numbers of tokens and K that is no whole number of blocks;
+# test_abi_fp8.py holds the lists against the rule.
+LINEAR_VARIANTS = [
+    (13, 144, 136, 16, 1), (3, 400, 264, 16, 2), (16, 784, 136, 16, 3), (1, 1040, 1000, 16, 4), (5, 2064, 136, 16, 6),
+    (9, 5200, 392, 16, 8), (17, 16, 264, 32, 1), (31, 400, 136, 32, 2), (19, 784, 264, 32, 3), (32, 1040, 136, 32, 4),
+    (23, 2064, 264, 32, 6), (29, 5200, 136, 32, 8), (33, 144, 136, 48, 1), (47, 400, 264, 48, 2), (35, 784, 136, 48, 3),
+    (48, 1040, 264, 48, 4), (41, 2064, 136, 48, 6), (45, 5200, 264, 48, 8), (49, 16, 136, 64, 1), (63, 400, 264, 64, 2),
+    (101, 656, 136, 64, 3), (64, 912, 264, 64, 4), (57, 1440, 136, 64, 6), (50, 4016, 264, 64, 8), (65, 144, 8440, 96, 1),
+    (782, 400, 640, 96, 2), (516, 656, 632, 96, 3), (643, 912, 384, 96, 4), (323, 1440, 504, 96, 6), (337, 4000, 376, 96, 8),
+    (969, 656, 888, 128, 2), (778, 1040, 632, 128, 3), (971, 912, 504, 128, 4), (485, 3600, 376, 128, 6),
+    (391, 4048, 376, 128, 8), (51, 16, 16640, 0, 1), (1500, 272, 2056, 0, 1)]
+SWIGLU_VARIANTS = [
+    (13, 144, 128, 16, 1), (3, 400, 256, 16, 2), (16, 784, 128, 16, 3), (1, 1040, 256, 16, 4), (5, 2064, 128, 16, 6),
+    (9, 5200, 128, 16, 8), (17, 16, 256, 32, 1), (31, 400, 128, 32, 2), (19, 784, 256, 32, 3), (32, 1040, 128, 32, 4),
+    (23, 2064, 128, 32, 6), (29, 5200, 256, 32, 8), (33, 144, 128, 48, 1), (47, 400, 256, 48, 2), (35, 784, 128, 48, 3),
+    (48, 1040, 256, 48, 4), (41, 2064, 128, 48, 6), (45, 5200, 128, 48, 8), (49, 16, 9600, 64, 1), (651, 672, 512, 64, 2),
+    (101, 656, 256, 64, 3), (64, 912, 128, 64, 4), (57, 1424, 128, 64, 6), (50, 3984, 128, 64, 8), (275, 128, 4864, 96, 1),
+    (65, 16, 9600, 96, 1), (897, 3264, 640, 96, 2), (975, 1840, 384, 96, 3), (897, 1296, 384, 96, 4), (583, 5152, 256, 96, 6),
+    (517, 4016, 256, 96, 8), (1173, 7232, 512, 128, 3), (1013, 5632, 512, 128, 4), (489, 14032, 384, 128, 8),
+    (49, 16, 128, 0, 1), (700, 256, 1280, 0, 1)]
+
+
+@pytest.mark.parametrize("M,K,N,tile,splits", LINEAR_VARIANTS)
+def test_linear_in_every_variant(h3q, cuda_device, M, K, N, tile, splits):
+    test_linear_within_bound(h3q, cuda_device, M, K, N)
+
+
+@pytest.mark.parametrize("M,K,F,tile,splits", SWIGLU_VARIANTS)
+def test_swiglu_in_every_variant(h3q, cuda_device, M, K, F, tile, splits):
+    test_swiglu_within_bound(h3q, cuda_device, M, K, F, M % 2 == 0)
+
+
 def test_scales_of_any_value_are_applied(h3q, cuda_device):
     """Negative, zero, huge and tiny scales, all codes: the product is what the operands say."""
     M, K, N = 70, 400, 264

@@ -48,6 +48,7 @@ _SIGS = {
     "h3q_fp8_prepare_weight": (_INT, [_P, _INT, _I64, _I64, _P, _P, _P]),
     "h3q_linear_fp8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P]),
     "h3q_linear_fp8_swiglu_quant": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P]),
+    "h3q_test_fp8_plan": (_INT, [_I64, _I64, _I64, _INT, _INT, _P]),
     "h3q_qk_norm_rope": (_INT, [_P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _I64,
                                 _I64, _INT, _P, _P, _P, _I64, _I64, _P]),
     "h3q_gemm_s32": (_INT, [_P, _P, _I64, _I64, _I64, _P, _P]),
@@ -452,6 +453,14 @@ def h3q_linear_fp8_swiglu_quant(xq, sx, wq, sw, hq, sh, bias=None, stream=None) 
     M, K, N, index = _fp8_operands(w, xq, sx, wq, sw, bias, hq, "e4m3", True, sh)
     _run(w, lib.h3q_linear_fp8_swiglu_quant, index, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(),
          sw.data_ptr(), N, _ptr(bias), hq.data_ptr(), sh.data_ptr())
+
+
+def h3q_test_fp8_plan(M, K, N, epilogue=H3Q_EPI_NONE, sms=148):
+    """(tokens of a tile, 0 for the large kernel; CTAs along K; stages; shared-memory bytes;
+    tensor-memory columns) of an fp8 product on a GPU of `sms` SMs. Host only."""
+    plan = (ctypes.c_int32 * 5)()
+    _check(lib.h3q_test_fp8_plan(M, K, N, int(epilogue), sms, plan), "h3q_test_fp8_plan")
+    return tuple(plan)
 
 
 H3Q_QK_MAX_D = 256

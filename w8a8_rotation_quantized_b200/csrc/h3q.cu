@@ -11,6 +11,7 @@
 #include <atomic>
 #include <mutex>
 #include <set>
+#include <type_traits>
 #include <utility>
 
 #include "h3q.h"
@@ -228,12 +229,14 @@ h3q_status launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned threa
   return H3Q_ERR_CUDA;
 }
 
-// How the kernel for few tokens would run: CTAs per tile along K, and an estimate of its
-// time in microseconds.
-struct Fp8SmallPlan {
-  int splits;
-  bool two;  // two CTAs an SM
-  double us;
+// How an fp8 product runs.
+struct Fp8Plan {
+  int tile;    // tokens of a tile of the kernel for few tokens; 0: the large kernel
+  int splits;  // CTAs per tile along K
+  int stages;  // ring depth
+  size_t smem;
+  int tmem;    // tensor-memory columns of a CTA
+  double us;   // estimated time
 };
 
 // Which fp8 product runs is decided by estimates of their times, fitted to measured ones
@@ -247,7 +250,7 @@ struct Fp8SmallPlan {
 constexpr double kF8LargeStepUs = 0.39, kF8LargeFixedUs = 5.0, kF8LargeRoundUs = 2.1;
 
 template <int R, int TM>
-Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
+Fp8Plan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
   constexpr double kStepUs = R == 1 ? (TM == 128 ? 0.525 : TM == 96 ? 0.475 : 0.40) : (TM == 128 ? 0.935 : TM == 96 ? 0.66 : 0.575);
   constexpr double kFixedUs = R == 1 ? (TM == 128 ? 4.9 : 4.3) : (TM == 128 ? 7.5 : TM == 96 ? 6.2 : 5.2);
   constexpr double kRoundUs = R == 1 ? (TM == 128 ? 5.5 : TM == 96 ? 4.9 : 2.0) : (TM == 128 ? 8.7 : TM == 96 ? 7.1 : 6.2);
@@ -261,7 +264,8 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
   // instead of 18). One token, K 5376, in a graph: N 5376 split six ways 9.3 us, four
   // 9.0, not 18.1; N 16128 two 17.4, not 19.2; SwiGLU to 14336 not 27.0, two 27.6.
   const bool fits_two = R * TM <= 64;
-  Fp8SmallPlan pl{1, false, 0.0};
+  using Cfg = h3q::Fp8Small<R, TM>;
+  Fp8Plan pl{TM, 1, 0, 0, Cfg::kTmem, 0.0};
   for (const int s : {2, 3, 4, 6, 8}) {
     int64_t most = fits_two ? (s == 8 ? int64_t(sms) * 4 / 3 : int64_t(sms) * 7 / 4)
                             : (s == 2 ? int64_t(sms) : s <= 4 ? int64_t(sms) * 7 / 8 : int64_t(sms) * 2 / 3);
@@ -271,7 +275,10 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
   // Half of an SM's shared memory for the ring where two CTAs fit, so that the next
   // launch's find room beside this one's; all of it for the long streams of an unsplit
   // gate/up product (27.0 against 29.2 us).
-  pl.two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
+  const bool two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
+  const int64_t room = ((two ? 113 : 226) * 1024 - Cfg::kFixed) / Cfg::kStage;
+  pl.stages = static_cast<int>(std::min(std::min(room, int64_t(h3q::kF8sMaxStages)), std::max(int64_t(3), (KB + pl.splits - 1) / pl.splits)));
+  pl.smem = size_t(pl.stages) * Cfg::kStage + Cfg::kFixed;
   const int64_t ctas = tiles * pl.splits, rounds = (ctas + sms - 1) / sms;
   pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs + kFixedUs + double(rounds - 1) * kRoundUs +
           (pl.splits > 1 ? 0.25 : 0.0) + (pl.splits >= 6 ? 0.5 : 0.0);
@@ -283,9 +290,8 @@ Fp8SmallPlan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) 
 template <int EPI, int TM>
 h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w,
                                  const float* sw, int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
-                                 const Fp8SmallPlan& plan, cudaStream_t stream) {
+                                 const Fp8Plan& plan, cudaStream_t stream) {
   constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
-  using Cfg = h3q::Fp8Small<R, TM>;
   CUtensorMap tw, tx;
   const int64_t num_m = (M + TM - 1) / TM;
   const int x_rows = static_cast<int>((M + num_m - 1) / num_m);
@@ -307,14 +313,11 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   p.sh = sh;
   p.wait_limit_ns = g_wait_limit_ns.load();
   const int64_t tiles = int64_t(p.num_m) * p.num_n;
-  const int splits = plan.splits;
-  p.splits = splits;
+  p.splits = plan.splits;
   p.x_rows = x_rows;
-  const int room = (plan.two ? 113 * 1024 : 226 * 1024) - Cfg::kFixed;
-  p.stages = std::min(std::min(room / Cfg::kStage, h3q::kF8sMaxStages), std::max(3, (p.KB + splits - 1) / splits));
-  const size_t smem = size_t(p.stages) * Cfg::kStage + Cfg::kFixed;
-  return launch_dependent(h3q::gemm_fp8_small_kernel<EPI, TM>, dim3(static_cast<unsigned>(tiles * splits)),
-                          h3q::kF8sThreads, smem, static_cast<unsigned>(splits), stream, tw, tx, p);
+  p.stages = plan.stages;
+  return launch_dependent(h3q::gemm_fp8_small_kernel<EPI, TM>, dim3(static_cast<unsigned>(tiles * plan.splits)),
+                          h3q::kF8sThreads, plan.smem, static_cast<unsigned>(plan.splits), stream, tw, tx, p);
 }
 
 template <int EPI>
@@ -362,38 +365,46 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
                           tout, p);
 }
 
+// R: 1, or 2 with SwiGLU.
+template <int R>
+Fp8Plan plan_gemm_fp8(int64_t M, int64_t K, int64_t N_out, int sms) {
+  const int64_t KB = (K + 127) / 128;
+  if (M <= 16) return plan_gemm_fp8_small<R, 16>(M, N_out, KB, sms);
+  if (M <= 32) return plan_gemm_fp8_small<R, 32>(M, N_out, KB, sms);
+  if (M <= 48) return plan_gemm_fp8_small<R, 48>(M, N_out, KB, sms);
+  const int64_t tiles = ((M + 255) / 256) * (R == 1 ? (N_out + 255) / 256 : N_out / 128);
+  const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2);
+  const Fp8Plan large{0, 1, h3q::kF8Stages, h3q::kF8Smem, h3q::kTmemCols,
+                      double(rounds) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs + double(rounds - 1) * kF8LargeRoundUs};
+  Fp8Plan best = plan_gemm_fp8_small<R, 64>(M, N_out, KB, sms);
+  if (M > 64) {
+    const Fp8Plan p96 = plan_gemm_fp8_small<R, 96>(M, N_out, KB, sms);
+    const Fp8Plan p128 = plan_gemm_fp8_small<R, 128>(M, N_out, KB, sms);
+    if (p96.us < best.us) best = p96;
+    if (p128.us < best.us) best = p128;
+  }
+  return best.us <= large.us ? best : large;
+}
+
 template <int EPI>
 h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w, const float* sw,
                            int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
                            cudaStream_t stream) {
-  constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
-  const int64_t KB = (K + 127) / 128;
-  if (M <= 16)
-    return launch_gemm_fp8_small<EPI, 16>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
-                                          plan_gemm_fp8_small<R, 16>(M, N_out, KB, sms), stream);
-  if (M <= 32)
-    return launch_gemm_fp8_small<EPI, 32>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
-                                          plan_gemm_fp8_small<R, 32>(M, N_out, KB, sms), stream);
-  if (M <= 48)
-    return launch_gemm_fp8_small<EPI, 48>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh,
-                                          plan_gemm_fp8_small<R, 48>(M, N_out, KB, sms), stream);
-  const int64_t large_tiles = ((M + 255) / 256) * (R == 1 ? (N_out + 255) / 256 : N_out / 128);
-  const int64_t large_rounds = (large_tiles + sms / 2 - 1) / (sms / 2);
-  const double large_us = double(large_rounds) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs + double(large_rounds - 1) * kF8LargeRoundUs;
-  const Fp8SmallPlan p64 = plan_gemm_fp8_small<R, 64>(M, N_out, KB, sms);
-  const Fp8SmallPlan p96 = plan_gemm_fp8_small<R, 96>(M, N_out, KB, sms);
-  const Fp8SmallPlan p128 = plan_gemm_fp8_small<R, 128>(M, N_out, KB, sms);
-  const double least = M <= 64 ? p64.us : std::min(std::min(p64.us, p96.us), p128.us);
-  if (least <= large_us) {
-    if (least == p64.us)
-      return launch_gemm_fp8_small<EPI, 64>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p64, stream);
-    if (least == p96.us)
-      return launch_gemm_fp8_small<EPI, 96>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p96, stream);
-    return launch_gemm_fp8_small<EPI, 128>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, p128, stream);
+  const Fp8Plan plan = plan_gemm_fp8<EPI == h3q::kF8BF16 ? 1 : 2>(M, K, N_out, sms);
+  auto few = [&](auto tile) {
+    return launch_gemm_fp8_small<EPI, decltype(tile)::value>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, plan, stream);
+  };
+  switch (plan.tile) {
+    case 16: return few(std::integral_constant<int, 16>{});
+    case 32: return few(std::integral_constant<int, 32>{});
+    case 48: return few(std::integral_constant<int, 48>{});
+    case 64: return few(std::integral_constant<int, 64>{});
+    case 96: return few(std::integral_constant<int, 96>{});
+    case 128: return few(std::integral_constant<int, 128>{});
+    default: return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
   }
-  return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
 }
 
 // Warps of qk_norm_rope wanted per SM: below that many tokens an SM, the heads of a
@@ -766,6 +777,18 @@ h3q_status h3q_linear_fp8_swiglu_quant(const uint8_t* xq, const float* sx, int64
   if (st != H3Q_OK || M == 0) return st;
   if (!hq || !sh || !aligned16(hq) || !aligned16(sh)) return H3Q_ERR_INVALID_ARG;
   return launch_gemm_fp8<h3q::kF8SwiGLUQuant>(xq, sx, M, K, wq, sw, N, N / 2, bias_bf16, hq, sh, stream);
+}
+
+h3q_status h3q_test_fp8_plan(int64_t M, int64_t K, int64_t N, int epilogue, int sms, int32_t* plan) {
+  if (M < 1 || !valid_fp8_k(K) || N <= 0 || N % 8 != 0 || sms < 2 || !plan) return H3Q_ERR_INVALID_ARG;
+  if (epilogue != H3Q_EPI_NONE && (epilogue != H3Q_EPI_SWIGLU || N % 256 != 0)) return H3Q_ERR_INVALID_ARG;
+  const Fp8Plan p = epilogue == H3Q_EPI_SWIGLU ? plan_gemm_fp8<2>(M, K, N / 2, sms) : plan_gemm_fp8<1>(M, K, N, sms);
+  plan[0] = p.tile;
+  plan[1] = p.splits;
+  plan[2] = p.stages;
+  plan[3] = static_cast<int32_t>(p.smem);
+  plan[4] = p.tmem;
+  return H3Q_OK;
 }
 
 h3q_status h3q_qk_norm_rope(const void* q, const void* k, int64_t S, int64_t Hq, int64_t Hk, int64_t D, int64_t ldq,
