@@ -152,3 +152,13 @@ def test_every_variant_of_the_products_is_tested(epilogue):
     picked = {h3q.h3q_test_fp8_plan(M, K, N, epilogue)[:2] for M, K, N in _sizes(epilogue)}
     assert picked <= {v[3:] for v in listed}
     assert {v[3] for v in listed} == {0, 16, 32, 48, 64, 96, 128}
+
+
+@pytest.mark.parametrize("epilogue", [h3q.H3Q_EPI_NONE, h3q.H3Q_EPI_SWIGLU])
+def test_no_product_waits_for_tensor_memory(epilogue):
+    """Blocks that fit an SM together (228 KB of shared memory, 1 KB of it kept for each block) hold
+    at most its 512 columns, whatever their kernels: each asks for the share of the shared memory
+    that its columns are of all columns."""
+    for M, K, N in _sizes(epilogue):
+        _, _, _, smem, columns = h3q.h3q_test_fp8_plan(M, K, N, epilogue)
+        assert columns * 228 * 1024 <= 512 * (smem + 1024) and smem <= 227 * 1024, (M, K, N, smem, columns)

@@ -295,6 +295,14 @@ __device__ __forceinline__ void f8_bias32(float* acc, const __nv_bfloat16* bias)
   for (int g = 0; g < 4; ++g) f8_bias8(acc + 8 * g, bias + 8 * g);
 }
 
+// tcgen05.alloc waits, without a limit, for columns that other CTAs of the SM hold, and a CTA
+// of a cluster frees its own only with its peers: CTAs of two clusters (of two streams, say)
+// that each held columns the other waits for would wait for ever. So every CTA of these
+// products asks for at least the share of the SM's shared memory that its columns are of the
+// SM's 512: CTAs that fit an SM together have their columns without a wait.
+constexpr int kSmShared = 228 * 1024, kSmSharedPerCta = 1024;  // an SM's, and what it keeps for each CTA
+__host__ __device__ constexpr int smem_for_tmem(int cols) { return cols * (kSmShared / 512) - kSmSharedPerCta; }
+
 enum Fp8Epi : int { kF8BF16 = 0, kF8SwiGLU = 1, kF8SwiGLUQuant = 2 };
 
 constexpr int64_t kF8MaxTiles = int64_t(1) << 23;  // output tiles of a call (the host refuses more)
@@ -313,7 +321,7 @@ constexpr int kF8ScaleSlot = 128 * 4 + 16;  // a K block's scales of the CTA's 1
 constexpr int kF8OutTile = 32 * 64;         // a warp's 32 output rows of 64 bytes
 constexpr size_t kF8Smem = size_t(kF8Stages) * kF8StageBytes + kF8Warps * 2 * kF8OutTile + kF8ScaleRing * kF8ScaleSlot +
                            2 * 4 * 128 * 4 /*row maxima*/ + 256 /*barriers*/ + 1024 /*align*/;
-static_assert(kF8Smem <= 232448, "shared memory of one CTA");
+static_assert(kF8Smem <= smem_for_tmem(kTmemCols), "shared memory of one CTA");
 // Register split: the launch's 96 per thread, moved from the control warps to the
 // ones that hold accumulators.
 constexpr uint32_t kF8RegsCtl = 32, kF8RegsPromote = 112, kF8RegsLaunch = 96;
@@ -746,15 +754,16 @@ struct Fp8Small {
   static constexpr int kCols = R * TM;                       // tensor-memory columns of one K block
   static constexpr int kHalf = kCols / 2;                    // columns of a promotion thread
   static constexpr int kBufs = kCols > 128 ? 2 : 4;
-  // Tensor memory is allocated by powers of two. CTAs of any variants that share an SM (by
-  // registers) need 512 columns together at most, so no allocation waits for a CTA whose
-  // cluster waits for this one.
   static constexpr int kTmem = kCols * kBufs <= 64 ? 64 : kCols * kBufs <= 128 ? 128 : kCols * kBufs <= 256 ? 256 : 512;
   static constexpr int kPartials = R * TM * 128 * 4;
   static_assert(kPartials <= 3 * kStage, "the partial sums fit in the operand ring");
   static constexpr int kScaleSlot = TM * 4 + 16;
   static constexpr int kFixed = kF8sScaleRing * kScaleSlot + 512 /*barriers*/ + 1024 /*align*/;
 };
+// Nor does one of these CTAs, the smallest of three stages, fit beside a CTA of the other
+// products whose clusters wait for all 512 columns.
+static_assert(3 * Fp8Small<1, 16>::kStage + Fp8Small<1, 16>::kFixed + (kGemmSmem < kF4Smem ? kGemmSmem : kF4Smem) +
+                      2 * kSmSharedPerCta > kSmShared, "tensor memory without a wait");
 
 struct Fp8SmallParams {
   int M, N, KB;

@@ -234,7 +234,7 @@ struct Fp8Plan {
   int tile;    // tokens of a tile of the kernel for few tokens; 0: the large kernel
   int splits;  // CTAs per tile along K
   int stages;  // ring depth
-  size_t smem;
+  int smem;    // bytes of shared memory
   int tmem;    // tensor-memory columns of a CTA
   double us;   // estimated time
 };
@@ -278,7 +278,7 @@ Fp8Plan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
   const bool two = fits_two && !(R == 2 && pl.splits == 1 && tiles <= sms);
   const int64_t room = ((two ? 113 : 226) * 1024 - Cfg::kFixed) / Cfg::kStage;
   pl.stages = static_cast<int>(std::min(std::min(room, int64_t(h3q::kF8sMaxStages)), std::max(int64_t(3), (KB + pl.splits - 1) / pl.splits)));
-  pl.smem = size_t(pl.stages) * Cfg::kStage + Cfg::kFixed;
+  pl.smem = std::max(pl.stages * Cfg::kStage + Cfg::kFixed, h3q::smem_for_tmem(Cfg::kTmem));
   const int64_t ctas = tiles * pl.splits, rounds = (ctas + sms - 1) / sms;
   pl.us = double(rounds) * double((KB + pl.splits - 1) / pl.splits) * kStepUs + kFixedUs + double(rounds - 1) * kRoundUs +
           (pl.splits > 1 ? 0.25 : 0.0) + (pl.splits >= 6 ? 0.5 : 0.0);
@@ -297,7 +297,7 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   const int x_rows = static_cast<int>((M + num_m - 1) / num_m);
   if (!make_tmap_i8(&tw, w, w_rows, K) || !make_tmap_i8(&tx, x, M, K, x_rows)) return H3Q_ERR_CUDA;
   const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_small_kernel<EPI, TM>);
-  if (ensure_smem_attr(kernel, 232448) != cudaSuccess) return H3Q_ERR_CUDA;
+  if (ensure_smem_attr(kernel, h3q::smem_for_tmem(512)) != cudaSuccess) return H3Q_ERR_CUDA;
   h3q::Fp8SmallParams p{};
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N_out);
@@ -323,13 +323,13 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
 template <int EPI>
 h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, int64_t K, const uint8_t* b, const float* sw,
                            int64_t b_rows, int64_t N_out, const void* bias, void* out, float* sh,
-                           cudaStream_t stream) {
+                           const Fp8Plan& plan, cudaStream_t stream) {
   CUtensorMap ta, tb, tout;
   if (!make_tmap_i8(&ta, a, M, K) || !make_tmap_i8(&tb, b, b_rows, K) ||
       !make_tmap_f8_out(&tout, out, M, N_out, EPI == h3q::kF8SwiGLUQuant))
     return H3Q_ERR_CUDA;
   const void* kernel = reinterpret_cast<const void*>(h3q::gemm_fp8_kernel<EPI>);
-  if (ensure_smem_attr(kernel, static_cast<int>(h3q::kF8Smem)) != cudaSuccess) return H3Q_ERR_CUDA;
+  if (ensure_smem_attr(kernel, plan.smem) != cudaSuccess) return H3Q_ERR_CUDA;
   // the kernel's register split assumes this many registers per thread at launch
   static std::once_flag regs_once;
   static bool regs_ok = false;
@@ -361,7 +361,7 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
-  return launch_dependent(h3q::gemm_fp8_kernel<EPI>, dim3(2 * pairs), h3q::kF8Threads, h3q::kF8Smem, 0, stream, ta, tb,
+  return launch_dependent(h3q::gemm_fp8_kernel<EPI>, dim3(2 * pairs), h3q::kF8Threads, plan.smem, 0, stream, ta, tb,
                           tout, p);
 }
 
@@ -374,7 +374,7 @@ Fp8Plan plan_gemm_fp8(int64_t M, int64_t K, int64_t N_out, int sms) {
   if (M <= 48) return plan_gemm_fp8_small<R, 48>(M, N_out, KB, sms);
   const int64_t tiles = ((M + 255) / 256) * (R == 1 ? (N_out + 255) / 256 : N_out / 128);
   const int64_t rounds = (tiles + sms / 2 - 1) / (sms / 2);
-  const Fp8Plan large{0, 1, h3q::kF8Stages, h3q::kF8Smem, h3q::kTmemCols,
+  const Fp8Plan large{0, 1, h3q::kF8Stages, h3q::smem_for_tmem(h3q::kTmemCols), h3q::kTmemCols,
                       double(rounds) * double(KB) * kF8LargeStepUs + kF8LargeFixedUs + double(rounds - 1) * kF8LargeRoundUs};
   Fp8Plan best = plan_gemm_fp8_small<R, 64>(M, N_out, KB, sms);
   if (M > 64) {
@@ -403,7 +403,7 @@ h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t
     case 64: return few(std::integral_constant<int, 64>{});
     case 96: return few(std::integral_constant<int, 96>{});
     case 128: return few(std::integral_constant<int, 128>{});
-    default: return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, stream);
+    default: return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, plan, stream);
   }
 }
 
@@ -786,7 +786,7 @@ h3q_status h3q_test_fp8_plan(int64_t M, int64_t K, int64_t N, int epilogue, int 
   plan[0] = p.tile;
   plan[1] = p.splits;
   plan[2] = p.stages;
-  plan[3] = static_cast<int32_t>(p.smem);
+  plan[3] = p.smem;
   plan[4] = p.tmem;
   return H3Q_OK;
 }
