@@ -339,10 +339,11 @@ h3q_status h3q_gemm_s32(const int8_t* xq, const int8_t* wq, int64_t M, int64_t N
 h3q_status h3q_get_device_status(cudaStream_t stream);
 
 /*
- * Upper bound, in nanoseconds, on every spin-wait inside the GEMM kernel (an
+ * Upper bound, in nanoseconds, on every spin-wait inside the kernels (an
  * mbarrier the kernel waits on). Past it the kernel records H3Q_ERR_TIMEOUT,
- * drains its own copies in flight (again bounded), frees its tensor memory and
- * returns. Default 2 s. Values below 1000 ns are raised to 1000 ns.
+ * drains its own copies in flight (again bounded, by this limit or 20 ms,
+ * whichever is longer), frees its tensor memory and returns. Default 2 s. Values
+ * below 1000 ns are raised to 1000 ns.
  */
 void h3q_set_wait_limit_ns(uint64_t ns);
 
@@ -354,6 +355,16 @@ void h3q_set_wait_limit_ns(uint64_t ns);
  * h3q_get_device_status returns H3Q_ERR_TIMEOUT. No fault, no hang.
  */
 h3q_status h3q_test_stalled_wait(uint64_t limit_ns, cudaStream_t stream);
+
+/*
+ * Test hook for the bounded waits of the fp8 products: h3q_linear_fp8 without a bias,
+ * whose operand tiles never count as complete, with the given limit. It returns as any
+ * call does; y is left undefined, and afterwards h3q_get_device_status returns
+ * H3Q_ERR_TIMEOUT. No fault, no hang.
+ */
+h3q_status h3q_test_stalled_linear_fp8(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq,
+                                       const float* sw, int64_t N, int epilogue, void* y_bf16, uint64_t limit_ns,
+                                       cudaStream_t stream);
 
 /* Human-readable name of a status code (static string). */
 const char* h3q_status_string(h3q_status s);

@@ -162,3 +162,15 @@ def test_no_product_waits_for_tensor_memory(epilogue):
     for M, K, N in _sizes(epilogue):
         _, _, _, smem, columns = h3q.h3q_test_fp8_plan(M, K, N, epilogue)
         assert columns * 228 * 1024 <= 512 * (smem + 1024) and smem <= 227 * 1024, (M, K, N, smem, columns)
+
+
+def test_stalled_product_rejects():
+    f = h3q.lib.h3q_test_stalled_linear_fp8
+    ok = [FAKE, FAKE, 4, 512, FAKE, FAKE, 512, 0, FAKE, 1000, None]
+    for i, bad in [(0, None), (2, -1), (3, 8), (4, None), (6, 12), (7, 2), (8, None), (8, FAKE + 8), (9, 10**10 + 1)]:
+        args = list(ok)
+        args[i] = bad
+        assert f(*args) == INV, (i, bad)
+    args = list(ok)
+    args[6], args[7] = 384, h3q.H3Q_EPI_SWIGLU
+    assert f(*args) == INV

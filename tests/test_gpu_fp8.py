@@ -463,6 +463,23 @@ def test_large_products_back_to_back(h3q, cuda_device):
     assert h3q.h3q_get_device_status() == h3q.H3Q_OK
 
 
+@pytest.mark.parametrize("limit_ns", [0, 3_000_000])
+@pytest.mark.parametrize("M,K,N,epilogue", [(1, 16, 136, 0), (9, 5200, 392, 0), (128, 1040, 8440, 0), (23, 2064, 256, 1),
+                                            (489, 14032, 768, 1), (1500, 272, 2056, 0), (700, 1360, 2560, 1)])
+def test_waits_that_run_out(h3q, cuda_device, M, K, N, epilogue, limit_ns):
+    """Operands that never count as complete: each kernel gives up, waits for its own copies however
+    short the limit is, and says so; the same operands give the same result as ever afterwards."""
+    ops = _operands(h3q, M, K, N, 6, cuda_device, False)[:4]
+    want, y = (torch.zeros(M, N // 2 if epilogue else N, dtype=torch.bfloat16, device=cuda_device) for _ in range(2))
+    h3q.h3q_linear_fp8(*ops, want, epilogue=epilogue)
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+    h3q.h3q_test_stalled_linear_fp8(*ops, y, limit_ns, epilogue=epilogue)
+    h3q.h3q_linear_fp8(*ops, y, epilogue=epilogue)  # at once, behind the call that gave up
+    assert h3q.h3q_get_device_status() == h3q.H3Q_ERR_TIMEOUT
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK  # cleared
+    assert torch.equal(y, want)
+
+
 def _some(n):
     """Rows at both ends, and at and past element 2^31 of rows of 14336."""
     return torch.cat([torch.arange(0, 3), torch.arange(149795, 149799), torch.arange(n - 3, n)])

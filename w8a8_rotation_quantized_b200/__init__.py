@@ -49,6 +49,7 @@ _SIGS = {
     "h3q_linear_fp8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _INT, _P, _P]),
     "h3q_linear_fp8_swiglu_quant": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _P, _P, _P, _P]),
     "h3q_test_fp8_plan": (_INT, [_I64, _I64, _I64, _INT, _INT, _P]),
+    "h3q_test_stalled_linear_fp8": (_INT, [_P, _P, _I64, _I64, _P, _P, _I64, _INT, _P, _U64, _P]),
     "h3q_qk_norm_rope": (_INT, [_P, _P, _I64, _I64, _I64, _I64, _I64, _I64, _P, _P, ctypes.c_float, _P, _P, _I64,
                                 _I64, _INT, _P, _P, _P, _I64, _I64, _P]),
     "h3q_gemm_s32": (_INT, [_P, _P, _I64, _I64, _I64, _P, _P]),
@@ -535,6 +536,15 @@ def h3q_set_wait_limit_ns(ns: int) -> None:
 
 def h3q_test_stalled_wait(limit_ns: int, stream=None) -> None:
     _check(lib.h3q_test_stalled_wait(int(limit_ns), _stream(stream)), "h3q_test_stalled_wait")
+
+
+def h3q_test_stalled_linear_fp8(xq, sx, wq, sw, y, limit_ns, epilogue=H3Q_EPI_NONE, stream=None) -> None:
+    """h3q_linear_fp8 whose operands never count as complete: it gives up after limit_ns."""
+    w = "h3q_test_stalled_linear_fp8"
+    epilogue = int(epilogue)
+    M, K, N, index = _fp8_operands(w, xq, sx, wq, sw, None, y, "bf16", epilogue == H3Q_EPI_SWIGLU)
+    _run(w, lib.h3q_test_stalled_linear_fp8, index, stream, xq.data_ptr(), sx.data_ptr(), M, K, wq.data_ptr(),
+         sw.data_ptr(), N, epilogue, y.data_ptr(), int(limit_ns))
 
 
 def h3q_status_string(status: int) -> str:

@@ -340,6 +340,7 @@ struct Fp8Params {
   void* out;                // bf16 [M, N], or e4m3 codes
   float* sh;                // SwiGLUQuant: [F / 128, M]
   uint64_t wait_limit_ns;
+  uint32_t missing_bytes;   // zero; bytes that every stage waits for in vain (test of the waits)
 };
 
 // acc += part * f, 32 columns, two multiply-adds an instruction: the same rate as single
@@ -487,7 +488,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
           }
           const uint32_t full_leader = cluster_map(&full[stage], 0);
           if (one) {
-            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes);
+            if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kF8StageBytes + p.missing_bytes);
             tma_load_2d_pair(sA + stage * kAStage, &tmA, full_leader, kb * kBK, a_row, pol);
             tma_load_2d_pair(sB + stage * kBStage, &tmB, full_leader, kb * kBK, b_row, pol);
           }
@@ -498,14 +499,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
         }
       }
       if (rank == 0) {
-        // the last copies, which nobody else waits for where a role gave up (bounded, ignores abort)
+        // the last copies, which nobody else waits for where a role gave up (bounded, ignores
+        // abort; after one wait that ran out they all have had their time)
         for (int m = n - 1; m >= 0 && m >= n - kF8Stages; --m)
-          mbar_wait_bounded(&full[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr);
+          if (!mbar_wait_bounded(&full[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr)) break;
       }
       // The issuers' last arrivals at this CTA's `empty`. They come from the leader, and neither
       // `tfull` nor `drain` says that they have landed here: a CTA that left earlier would have
-      // them arrive in shared memory that is the next one's. One wait that runs out is enough:
-      // what it waited for does not come any more.
+      // them arrive in shared memory that is the next one's. Where a role gave up, this is also
+      // the time in which the peer's copies land.
       for (int m = n - 1; m >= 0 && m >= n - kF8Stages; --m)
         if (!mbar_wait_bounded(&empty[m % kF8Stages], static_cast<uint32_t>((m / kF8Stages) & 1), limit, nullptr)) break;
     } else if (warp == kF8Producer + 1) {
@@ -777,6 +779,7 @@ struct Fp8SmallParams {
   void* out;
   float* sh;
   uint64_t wait_limit_ns;
+  uint32_t missing_bytes;   // zero; bytes that every stage waits for in vain (test of the waits)
 };
 
 // D[tmem] (+)= A[smem] * B[smem]^T, e4m3 x e4m3 -> fp32, one CTA.
@@ -874,7 +877,7 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
     uint8_t* dst = ring + stage * Cfg::kStage;
     const uint64_t pol = policy_evict_normal();
     const int k = (kb0 + i) * 128;
-    mbar_arrive_expect_tx(&full[stage], R * 128 * 128 + p.x_rows * 128);
+    mbar_arrive_expect_tx(&full[stage], R * 128 * 128 + p.x_rows * 128 + p.missing_bytes);
     tma_load_2d(dst, &tmW, &full[stage], k, nt * 128, pol);
     if (R == 2) tma_load_2d(dst + 128 * 128, &tmW, &full[stage], k, p.up_row + nt * 128, pol);
     tma_load_2d(dst + R * 128 * 128, &tmX, &full[stage], k, mt * p.x_rows, pol);
@@ -924,9 +927,10 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
         phase ^= 1u;
       }
     }
-    // the last copies, which nobody else waits for where a role gave up (bounded, ignores abort)
+    // the last copies, which nobody else waits for where a role gave up (bounded, ignores
+    // abort; after one wait that ran out they all have had their time)
     for (int m = i - 1; m >= 0 && m >= i - S; --m)
-      mbar_wait_bounded(&full[m % S], static_cast<uint32_t>((m / S) & 1), limit, nullptr);
+      if (!mbar_wait_bounded(&full[m % S], static_cast<uint32_t>((m / S) & 1), limit, nullptr)) break;
   } else if (warp == 9) {
     // ------------------------------------------------------------ MMA issuer
     constexpr uint32_t idesc = idesc_fp8(128, TM);

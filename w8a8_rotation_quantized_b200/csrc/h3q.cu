@@ -239,6 +239,13 @@ struct Fp8Plan {
   double us;   // estimated time
 };
 
+// The limit of an fp8 product's waits, and the bytes that every stage of its operand ring
+// waits for in vain (zero but in the test of the waits).
+struct Fp8Waits {
+  uint64_t limit_ns = g_wait_limit_ns.load();
+  uint32_t missing_bytes = 0;
+};
+
 // Which fp8 product runs is decided by estimates of their times, fitted to measured ones
 // (330 random shapes of 49 to 1500 tokens, K to 14336, each by every kernel, in a graph; the
 // choice costs 1% over the best of them on the mean): the rounds over the SMs times the K
@@ -290,7 +297,7 @@ Fp8Plan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
 template <int EPI, int TM>
 h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w,
                                  const float* sw, int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
-                                 const Fp8Plan& plan, cudaStream_t stream) {
+                                 const Fp8Plan& plan, const Fp8Waits& waits, cudaStream_t stream) {
   constexpr int R = EPI == h3q::kF8BF16 ? 1 : 2;
   CUtensorMap tw, tx;
   const int64_t num_m = (M + TM - 1) / TM;
@@ -311,7 +318,8 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   p.out = out;
   p.sh = sh;
-  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.wait_limit_ns = waits.limit_ns;
+  p.missing_bytes = waits.missing_bytes;
   const int64_t tiles = int64_t(p.num_m) * p.num_n;
   p.splits = plan.splits;
   p.x_rows = x_rows;
@@ -323,7 +331,7 @@ h3q_status launch_gemm_fp8_small(const uint8_t* x, const float* sx, int64_t M, i
 template <int EPI>
 h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, int64_t K, const uint8_t* b, const float* sw,
                            int64_t b_rows, int64_t N_out, const void* bias, void* out, float* sh,
-                           const Fp8Plan& plan, cudaStream_t stream) {
+                           const Fp8Plan& plan, const Fp8Waits& waits, cudaStream_t stream) {
   CUtensorMap ta, tb, tout;
   if (!make_tmap_i8(&ta, a, M, K) || !make_tmap_i8(&tb, b, b_rows, K) ||
       !make_tmap_f8_out(&tout, out, M, N_out, EPI == h3q::kF8SwiGLUQuant))
@@ -357,7 +365,8 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
   p.bias = static_cast<const __nv_bfloat16*>(bias);
   p.out = out;
   p.sh = sh;
-  p.wait_limit_ns = g_wait_limit_ns.load();
+  p.wait_limit_ns = waits.limit_ns;
+  p.missing_bytes = waits.missing_bytes;
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
   const int pairs = p.num_tiles < sms / 2 ? p.num_tiles : sms / 2;
@@ -389,12 +398,12 @@ Fp8Plan plan_gemm_fp8(int64_t M, int64_t K, int64_t N_out, int sms) {
 template <int EPI>
 h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t K, const uint8_t* w, const float* sw,
                            int64_t w_rows, int64_t N_out, const void* bias, void* out, float* sh,
-                           cudaStream_t stream) {
+                           cudaStream_t stream, const Fp8Waits& waits = {}) {
   const int sms = sm_count();
   if (sms <= 0) return H3Q_ERR_CUDA;
   const Fp8Plan plan = plan_gemm_fp8<EPI == h3q::kF8BF16 ? 1 : 2>(M, K, N_out, sms);
   auto few = [&](auto tile) {
-    return launch_gemm_fp8_small<EPI, decltype(tile)::value>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, plan, stream);
+    return launch_gemm_fp8_small<EPI, decltype(tile)::value>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, plan, waits, stream);
   };
   switch (plan.tile) {
     case 16: return few(std::integral_constant<int, 16>{});
@@ -403,7 +412,7 @@ h3q_status launch_gemm_fp8(const uint8_t* x, const float* sx, int64_t M, int64_t
     case 64: return few(std::integral_constant<int, 64>{});
     case 96: return few(std::integral_constant<int, 96>{});
     case 128: return few(std::integral_constant<int, 128>{});
-    default: return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, plan, stream);
+    default: return launch_gemm_fp8_large<EPI>(x, sx, M, K, w, sw, w_rows, N_out, bias, out, sh, plan, waits, stream);
   }
 }
 
@@ -777,6 +786,20 @@ h3q_status h3q_linear_fp8_swiglu_quant(const uint8_t* xq, const float* sx, int64
   if (st != H3Q_OK || M == 0) return st;
   if (!hq || !sh || !aligned16(hq) || !aligned16(sh)) return H3Q_ERR_INVALID_ARG;
   return launch_gemm_fp8<h3q::kF8SwiGLUQuant>(xq, sx, M, K, wq, sw, N, N / 2, bias_bf16, hq, sh, stream);
+}
+
+h3q_status h3q_test_stalled_linear_fp8(const uint8_t* xq, const float* sx, int64_t M, int64_t K, const uint8_t* wq,
+                                       const float* sw, int64_t N, int epilogue, void* y_bf16, uint64_t limit_ns,
+                                       cudaStream_t stream) {
+  if (limit_ns > 10000000000ull) return H3Q_ERR_INVALID_ARG;  // at most 10 s
+  if (epilogue != H3Q_EPI_NONE && (epilogue != H3Q_EPI_SWIGLU || N % 256 != 0)) return H3Q_ERR_INVALID_ARG;
+  const h3q_status st = check_fp8_args(xq, sx, M, K, wq, sw, N, nullptr);
+  if (st != H3Q_OK || M == 0) return st;
+  if (!y_bf16 || !aligned16(y_bf16)) return H3Q_ERR_INVALID_ARG;
+  const Fp8Waits waits{limit_ns < 1000 ? 1000 : limit_ns, 16};
+  if (epilogue == H3Q_EPI_SWIGLU)
+    return launch_gemm_fp8<h3q::kF8SwiGLU>(xq, sx, M, K, wq, sw, N, N / 2, nullptr, y_bf16, nullptr, stream, waits);
+  return launch_gemm_fp8<h3q::kF8BF16>(xq, sx, M, K, wq, sw, N, N, nullptr, y_bf16, nullptr, stream, waits);
 }
 
 h3q_status h3q_test_fp8_plan(int64_t M, int64_t K, int64_t N, int epilogue, int sms, int32_t* plan) {

@@ -78,10 +78,16 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // Waits until the phase with the given parity of `bar` has completed, or until
 // `limit_ns` has passed, or until *abort becomes nonzero. Returns true when the
 // phase completed. On expiry it records the timeout in g_status and raises
-// *abort so the other roles of the block stop too.
+// *abort so the other roles of the block stop too. Without *abort it is the wait
+// for a block's own copies and MMAs in flight before the block leaves, which must
+// not be cut short however small the caller's limit is: it lasts kDrainNs at least,
+// a thousand times what a copy takes.
+constexpr uint64_t kDrainNs = 20000000;
+
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                   volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
+  if (abort == nullptr && limit_ns < kDrainNs) limit_ns = kDrainNs;
   const uint64_t t0 = globaltimer_ns();
   uint32_t spins = 0;
   while (true) {
