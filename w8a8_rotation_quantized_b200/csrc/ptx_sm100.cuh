@@ -8,6 +8,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <cstddef>
+
 namespace h3q {
 
 // Device status word: nonzero once any bounded wait of this library expired.
@@ -78,16 +80,10 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 // Waits until the phase with the given parity of `bar` has completed, or until
 // `limit_ns` has passed, or until *abort becomes nonzero. Returns true when the
 // phase completed. On expiry it records the timeout in g_status and raises
-// *abort so the other roles of the block stop too. Without *abort it is the wait
-// for a block's own copies and MMAs in flight before the block leaves, which must
-// not be cut short however small the caller's limit is: it lasts kDrainNs at least,
-// a thousand times what a copy takes.
-constexpr uint64_t kDrainNs = 20000000;
-
+// *abort so the other roles of the block stop too.
 __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns,
                                                   volatile int* abort) {
   if (mbar_try_wait(bar, parity)) return true;
-  if (abort == nullptr && limit_ns < kDrainNs) limit_ns = kDrainNs;
   const uint64_t t0 = globaltimer_ns();
   uint32_t spins = 0;
   while (true) {
@@ -101,6 +97,17 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity
       }
     }
   }
+}
+
+// The same without an abort flag: a block's wait for its own copies and MMAs in flight
+// before it leaves. The caller's limit may be as short as a microsecond; this wait lasts
+// kDrainNs at least, a thousand times what a copy takes.
+constexpr uint64_t kDrainNs = 20000000;
+
+__host__ __device__ inline uint64_t drain_ns(uint64_t limit_ns) { return limit_ns > kDrainNs ? limit_ns : kDrainNs; }
+
+__device__ __forceinline__ bool mbar_wait_bounded(uint64_t* bar, uint32_t parity, uint64_t limit_ns, std::nullptr_t) {
+  return mbar_wait_bounded(bar, parity, drain_ns(limit_ns), static_cast<volatile int*>(nullptr));
 }
 
 // mbar_wait_bounded for waits that many threads make at once (the consumers of

@@ -335,6 +335,7 @@ struct RqArgs {
   int8_t* q;
   float* s_out;
   uint64_t wait_limit_ns;
+  uint64_t drain_limit_ns;  // of the waits for the block's own copies (from the host: in the kernel it spills registers)
   uint32_t tmem_cols;    // tensor-memory columns a block allocates (tensor-memory variant)
 };
 
@@ -433,7 +434,8 @@ __global__ void __launch_bounds__(GPS == 1 ? 768 : 512, 1)
         for (int s = 0; s < a.stages; ++s) {
           if (issued <= s) continue;
           const long last = ((issued - 1 - s) / a.stages) * a.stages + s;
-          mbar_wait_bounded(&full[s], static_cast<uint32_t>((last / a.stages) & 1), a.wait_limit_ns, nullptr);
+          mbar_wait_bounded(&full[s], static_cast<uint32_t>((last / a.stages) & 1), a.drain_limit_ns,
+                            static_cast<volatile int*>(nullptr));
         }
       }
     }
@@ -604,7 +606,8 @@ __global__ void __launch_bounds__(32 * (kRqtMaxWarps + 1), 1)
         for (int s = 0; s < a.stages; ++s) {
           if (issued <= s) continue;
           const long last = ((issued - 1 - s) / a.stages) * a.stages + s;
-          mbar_wait_bounded(&full[s], static_cast<uint32_t>((last / a.stages) & 1), a.wait_limit_ns, nullptr);
+          mbar_wait_bounded(&full[s], static_cast<uint32_t>((last / a.stages) & 1), a.drain_limit_ns,
+                            static_cast<volatile int*>(nullptr));
         }
       }
     }
@@ -860,6 +863,7 @@ RqArgs rotquant_args(const RqShape& sh, int64_t rows, int64_t K, int8_t* q, floa
   a.q = q;
   a.s_out = s;
   a.wait_limit_ns = wait_limit_ns;
+  a.drain_limit_ns = drain_ns(wait_limit_ns);
   a.tmem_cols = rotquant_tm_cols(sh.warps, sh.gps);
   return a;
 }
