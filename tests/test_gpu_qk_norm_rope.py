@@ -130,6 +130,33 @@ def test_nan_and_infinity_stay_in_their_heads(h3q, cuda_device):
     assert torch.equal(out.view(S, H, D)[keep], clean.view(S, H, D)[keep])
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_infinity_past_the_rotated_part(h3q, cuda_device, inter, weighted):
+    """Past the rotated elements nothing meets another element: an infinity makes the mean infinite,
+    so its own element NaN and every other one 0, and an infinite weight reaches its own element."""
+    S, H, D, rot = 5, 3, 80, 32
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn(S, H * D, generator=g).bfloat16().to(cuda_device)
+    w = torch.rand(D, generator=g).add(0.5).bfloat16().to(cuda_device)
+    cos, sin = _tables(S, rot, cuda_device)
+    at = [(0, 0, rot, "inf"), (1, 2, D - 1, "-inf"), (3, 1, 48, "inf"), (4, 0, 33, "-inf")]
+    for t, h, i, v in at:
+        x[t, h * D + i] = float(v)
+    out = torch.empty_like(x)
+    h3q.h3q_qk_norm_rope(x, None, H, 0, D, cos, sin, out, None, q_weight=w if weighted else None, interleaved=inter)
+    o = out.view(S, H, D)
+    for t, h, i, _ in at:
+        assert torch.isnan(o[t, h, i])
+        assert (torch.cat([o[t, h, :i], o[t, h, i + 1 :]]) == 0).all(), (t, h, i)
+    w[50] = float("inf")
+    x[:] = torch.randn(S, H * D, generator=g).bfloat16().to(cuda_device)
+    h3q.h3q_qk_norm_rope(x, None, H, 0, D, cos, sin, out, None, q_weight=w, interleaved=inter)
+    o = out.view(S, H, D)
+    assert torch.equal(o[:, :, 50], x.view(S, H, D)[:, :, 50] * float("inf"))
+    assert torch.isfinite(torch.cat([o[:, :, :50], o[:, :, 51:]], dim=2)).all()
+
+
 def test_strides_past_32_bits(h3q, cuda_device):
     """Row offsets beyond 2^32 elements: the last row of a [5, 2^30 + 64] view."""
     ld, S, H, D = 2**30 + 64, 5, 2, 64

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           cw[i] = __fmul2_rn(cw[i], make_float2(wi[2 * i], wi[2 * i + 1]));
-          sw[i] = __fmul2_rn(sw[i], INTER ? make_float2(wp[2 * i + 1], wp[2 * i]) : make_float2(wp[2 * i], wp[2 * i + 1]));
+          if (turns) sw[i] = __fmul2_rn(sw[i], INTER ? make_float2(wp[2 * i + 1], wp[2 * i]) : make_float2(wp[2 * i], wp[2 * i + 1]));
         }
       }
       uint4 next[kUnroll];
@@ -162,7 +162,13 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
             const uint32_t o = INTER ? w[i] : __shfl_sync(0xFFFFFFFFu, w[i], partner);
             const float2 xp = INTER ? make_float2(x[i].y, x[i].x)
                                     : make_float2(__uint_as_float(o << 16), __uint_as_float(o & 0xFFFF0000u));
-            y[i] = __fmul2_rn(__ffma2_rn(x[i], cw[i], __fmul2_rn(xp, sw[i])), make_float2(r, r));
+            if constexpr (INTER) {
+              y[i] = __fmul2_rn(x[i], cw[i]);
+              if (turns) y[i] = __ffma2_rn(xp, sw[i], y[i]);  // else no partner: 0 times its infinity is not 0
+            } else {  // past rot the partner is the element itself
+              y[i] = __ffma2_rn(x[i], cw[i], __fmul2_rn(xp, sw[i]));
+            }
+            y[i] = __fmul2_rn(y[i], make_float2(r, r));
           }
           if (live && h < H) {
             uint32_t out[4];
