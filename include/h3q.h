@@ -301,7 +301,8 @@ h3q_status h3q_test_fp8_plan(int64_t M, int64_t K, int64_t N, int epilogue, int 
  *   (interleaved == 0), or (2i, 2i + 1), of the first rot elements; the others are
  *   only normalised. c, s: row `position` of cos, sin [P, rot / 2] fp32; positions
  *   [S] int32, or NULL for positions 0, 1, ... (then P >= S). A position outside
- *   [0, P) reads no table row and leaves its token's rotated elements NaN.
+ *   [0, P) leaves its token's rotated elements NaN, whatever the tables hold.
+ *   The weight multiplies the table's c and s first (w c and w s finite in fp32).
  *   One rounding, to bf16 at the end. q_out, k_out [S, ld] may be q and k themselves
  *   (same pointer and stride); other overlaps are not supported. Columns outside
  *   the heads are neither read nor written.

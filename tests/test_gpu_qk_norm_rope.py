@@ -157,6 +157,32 @@ def test_infinity_past_the_rotated_part(h3q, cuda_device, inter, weighted):
     assert torch.isfinite(torch.cat([o[:, :, :50], o[:, :, 51:]], dim=2)).all()
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 64), (80, 32), (128, 128), (256, 128)])
+def test_large_elements_and_weights(h3q, cuda_device, inter, D, rot):
+    """Elements are divided by the root before a weight can carry them past the largest fp32: where
+    the squares' sum overflows (to a divided element of 0) and where it does not."""
+    S, H = 7, 3
+    g = torch.Generator().manual_seed(D)
+    x = torch.randn(S, H * D, generator=g).bfloat16().to(cuda_device)
+    cos, sin = _tables(S, rot, cuda_device)
+    x.view(S, H, D)[2, 1] = 3.3e38 * torch.sign(x.view(S, H, D)[2, 1])
+    x.view(S, H, D)[4, 0, D - 1] = -3.3e38
+    x.view(S, H, D)[5, 2, 3] = 1.5e19
+    w = (4 + torch.rand(D, generator=g)).bfloat16().to(cuda_device)
+    out = torch.empty_like(x)
+    h3q.h3q_qk_norm_rope(x, None, H, 0, D, cos, sin, out, None, q_weight=w, interleaved=inter)
+    o = out.view(S, H, D)
+    assert (o[2, 1] == 0).all() and (o[4, 0] == 0).all()
+    keep = torch.ones(S, H, dtype=torch.bool)
+    keep[2, 1] = keep[4, 0] = False
+    for big in (1.0, 2.0 ** 100):
+        w = (w.float() * big).bfloat16()
+        h3q.h3q_qk_norm_rope(x, None, H, 0, D, cos, sin, out, None, q_weight=w, interleaved=inter)
+        want, mag = (t.view(S, H, D)[keep] for t in _ref(x, H, D, w, cos, sin, rot, inter, None, 1e-6))
+        _close(o[keep], (want, mag))
+
+
 def test_strides_past_32_bits(h3q, cuda_device):
     """Row offsets beyond 2^32 elements: the last row of a [5, 2^30 + 64] view."""
     ld, S, H, D = 2**30 + 64, 5, 2, 64

@@ -8,12 +8,17 @@
 // A head is read by a group of lanes, eight elements (16 bytes) each; a warp works on
 // one token at a time, so its lanes load the token's table row once for all of its
 // heads and fold the norm's weights into it: with C_i = w_i c_i and S_i = -+w_p s_i (p
-// the partner of i), the result is r (x_i C_i + x_p S_i), three operations an element.
-// Six heads a lane group are worked on while the next six load (two blocks an SM: 114 us
-// at 84 heads of 128 over 16384 tokens; eight at once without loads ahead 124, four 149,
-// three or more blocks 120 to 135). Every element is read and written once and memory is
-// the bound: 713 MB there, 95% of the measured copy rate. Few tokens are spread over more
-// warps by splitting the heads.
+// the partner of i), the result is (x_i r) C_i + (x_p r) S_i. The root comes before the
+// weight, as in the formula: after it, a weight above one carried a large finite element
+// to infinity, and where the sum of squares overflows (r = 0) that gave NaN for 0. It costs
+// a multiplication for each pair of elements: 1% to 2% of the time with half-split pairs
+// (4% to 6% where everything is in L2), nothing with interleaved ones, whose partner is in
+// the same lane.
+// Six heads a lane group are worked on while the next six load (two blocks an SM: 117 us
+// at 84 heads of 128 over 16384 tokens, 115 interleaved or with the root last; with it last,
+// eight at once without loads ahead 124, four 149, three or more blocks 120 to 135). Every
+// element is read and written once and memory is the bound: 713 MB there, 93% of the
+// measured copy rate. Few tokens are spread over more warps by splitting the heads.
 //
 // A head's loads come before its stores and no head reads another's elements, so q_out
 // and k_out may be q and k themselves.
@@ -159,16 +164,15 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
           const float r = rsqrtf(__fmaf_rn(ss, inv_d, p.eps));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t o = INTER ? w[i] : __shfl_sync(0xFFFFFFFFu, w[i], partner);
-            const float2 xp = INTER ? make_float2(x[i].y, x[i].x)
-                                    : make_float2(__uint_as_float(o << 16), __uint_as_float(o & 0xFFFF0000u));
+            const float2 r2 = make_float2(r, r), n = __fmul2_rn(x[i], r2);
             if constexpr (INTER) {
-              y[i] = __fmul2_rn(x[i], cw[i]);
-              if (turns) y[i] = __ffma2_rn(xp, sw[i], y[i]);  // else no partner: 0 times its infinity is not 0
+              y[i] = __fmul2_rn(n, cw[i]);
+              if (turns) y[i] = __ffma2_rn(make_float2(n.y, n.x), sw[i], y[i]);  // else no partner: 0 times its infinity is not 0
             } else {  // past rot the partner is the element itself
-              y[i] = __ffma2_rn(x[i], cw[i], __fmul2_rn(xp, sw[i]));
+              const uint32_t o = __shfl_sync(0xFFFFFFFFu, w[i], partner);
+              const float2 np = __fmul2_rn(make_float2(__uint_as_float(o << 16), __uint_as_float(o & 0xFFFF0000u)), r2);
+              y[i] = __ffma2_rn(n, cw[i], __fmul2_rn(np, sw[i]));
             }
-            y[i] = __fmul2_rn(y[i], make_float2(r, r));
           }
           if (live && h < H) {
             uint32_t out[4];
