@@ -2,6 +2,7 @@
 them (or has nothing to do), so nothing is launched and no pointer is followed."""
 import ctypes
 import math
+import os
 import random
 
 import pytest
@@ -174,3 +175,11 @@ def test_stalled_product_rejects():
     args = list(ok)
     args[6], args[7] = 384, h3q.H3Q_EPI_SWIGLU
     assert f(*args) == INV
+
+
+@pytest.mark.parametrize("name", ["fp8.cuh", "qk_norm_rope.cuh"])
+def test_dependent_launches_read_no_memory_as_constant(name):
+    """These kernels may be resident while the calls before them still write, so they may not read
+    through the path for data that stays constant during a kernel."""
+    text = open(os.path.join(os.path.dirname(h3q.__file__), "csrc", name)).read()
+    assert "grid_dependency_wait();" in text and "__ldg" not in text and "ld.global.nc" not in text

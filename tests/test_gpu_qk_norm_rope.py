@@ -196,6 +196,42 @@ def test_strides_past_32_bits(h3q, cuda_device):
     assert torch.equal(big[:, 1024 : 1024 + H * D], out)
 
 
+@pytest.mark.parametrize("S", [1, 700])
+def test_operands_rewritten_by_the_calls_before(h3q, cuda_device, S):
+    """Tables, positions, norm weights and a product's bias are written anew, call after call, while
+    the dependents behind may be resident already: each call reads what was written before it."""
+    from test_gpu_fp8 import E4, _prepare, _quantize
+    H, D, K, rounds = 4, 64, 272, 12
+    dev = cuda_device
+    g = torch.Generator().manual_seed(S)
+    wq, sw = _prepare(h3q, torch.randn(2 * H * D, K, generator=g).to(dev))
+    xs = torch.randn(rounds, S, K, generator=g).bfloat16().to(dev)
+    tables = torch.rand(rounds, 2, 50, D // 2, generator=g).to(dev)
+    weights = torch.randn(rounds, D, generator=g).bfloat16().to(dev)
+    biases = torch.randn(rounds, 2 * H * D, generator=g).bfloat16().to(dev)
+    at = torch.randint(50, (rounds, S), generator=g, dtype=torch.int32).to(dev)
+    table, weight, bias, pos = (torch.empty_like(t[0]) for t in (tables, weights, biases, at))
+    xq, sx = _quantize(h3q, xs[0])
+    y = torch.empty(S, 2 * H * D, dtype=torch.bfloat16, device=dev)
+
+    def run(wait):
+        got = []
+        for i in range(rounds):
+            for to, of in ((table, tables), (weight, weights), (bias, biases), (pos, at)):
+                to.copy_(of[i])
+            for call in (lambda: h3q.h3q_fp8_quantize(xs[i], xq, sx), lambda: h3q.h3q_linear_fp8(xq, sx, wq, sw, y, bias=bias),
+                         lambda: h3q.h3q_qk_norm_rope(y[:, : H * D], y[:, H * D :], H, H, D, table[0], table[1], y[:, : H * D],
+                                                      y[:, H * D :], q_weight=weight, k_weight=weight, positions=pos)):
+                if wait:
+                    torch.cuda.synchronize()
+                call()
+            got.append(y.clone())
+        torch.cuda.synchronize()
+        return got
+
+    assert all(torch.equal(a, b) for a, b in zip(run(False), run(True)))
+
+
 def test_binding_refuses(h3q, cuda_device):
     x = torch.zeros(4, 256, dtype=torch.bfloat16, device=cuda_device)
     cos, sin = _tables(4, 64, cuda_device)

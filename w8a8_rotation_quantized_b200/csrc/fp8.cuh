@@ -57,15 +57,7 @@ __device__ __forceinline__ float fp8_scale(float a, float& inv) {
 
 // ---------------------------------------------------------------- quantize
 // Eight consecutive elements as fp32.
-__device__ __forceinline__ void fp8_load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
+__device__ __forceinline__ void fp8_load8(const __nv_bfloat16* p, float (&v)[8]) { load_bf16x8(p, v); }
 
 __device__ __forceinline__ void fp8_load8(const float* p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -1067,7 +1059,7 @@ __global__ void __launch_bounds__(kF8sThreads, (EPI == kF8BF16 ? TM : 2 * TM) <=
                            __fadd_rn(v[r].w, t.w));
       }
       if (p.bias != nullptr && n < p.N) {
-        const uint2 b = __ldg(reinterpret_cast<const uint2*>(p.bias + r * p.up_row + n));
+        const uint2 b = *reinterpret_cast<const uint2*>(p.bias + r * p.up_row + n);
         v[r].x = __fadd_rn(v[r].x, __uint_as_float(b.x << 16));
         v[r].y = __fadd_rn(v[r].y, __uint_as_float(b.x & 0xFFFF0000u));
         v[r].z = __fadd_rn(v[r].z, __uint_as_float(b.y << 16));

@@ -5,6 +5,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -173,6 +174,20 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // A block calls it with all that it has to allocate in hand, so that the dependent's
 // blocks can take none of it.
 __device__ __forceinline__ void grid_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Eight consecutive bf16 as fp32, by a plain load: a programmatic dependent is resident
+// while the calls before it may still be writing what it will read, so it reads nothing
+// through the read-only path (__ldg), which is for data that nobody writes during the
+// kernel's life.
+__device__ __forceinline__ void load_bf16x8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 a = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+  }
+}
 
 // ---------------------------------------------------------------- clusters
 __device__ __forceinline__ uint32_t cluster_ctarank() {

@@ -43,17 +43,6 @@ struct QkParams {
   float eps;
 };
 
-// Eight fp32 from eight consecutive bf16.
-__device__ __forceinline__ void qk_load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-  const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-  }
-}
-
 // G: lanes per head (a power of two, 8 G >= D). Grid: x tokens (warps stride over
 // them), y the part of the heads.
 template <int G, bool INTER>
@@ -86,8 +75,8 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
       constexpr int kVec = INTER ? 1 : 2;  // 16-byte pieces of the row
 #pragma unroll
       for (int v = 0; v < kVec; ++v) {
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(p.cos + off) + v);
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(p.sin + off) + v);
+        const float4 cv = reinterpret_cast<const float4*>(p.cos + off)[v];
+        const float4 sv = reinterpret_cast<const float4*>(p.sin + off)[v];
         const float cc[4] = {cv.x, cv.y, cv.z, cv.w}, ss[4] = {sv.x, sv.y, sv.z, sv.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -123,8 +112,8 @@ __global__ void __launch_bounds__(256, 2) qk_norm_rope_kernel(const QkParams p) 
       }
       if (wt != nullptr && live) {
         float wi[8], wp[8];
-        qk_load8(wt + 8 * l, wi);
-        qk_load8(wt + 8 * (partner % G), wp);
+        load_bf16x8(wt + 8 * l, wi);
+        load_bf16x8(wt + 8 * (partner % G), wp);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           cw[i] = __fmul2_rn(cw[i], make_float2(wi[2 * i], wi[2 * i + 1]));
