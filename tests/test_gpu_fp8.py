@@ -222,6 +222,62 @@ def test_swiglu_within_bound(h3q, cuda_device, M, K, F, with_bias):
     _close(back, h, e + half_step * (1 + 2.0 ** -20) + 2.0 ** -126)
 
 
+def _silu_of(h3q, gates, M, dev, up=1.0):
+    """silu(g) up of fp32 gates (repeated to M tokens) by the quantized product, as |h| from the scale
+    in 64 bits, and by the bf16 one. A one-hot code makes each token's gate its own scale, exactly."""
+    F = 1280
+    xq, wq = torch.zeros(M, 256, device=dev), torch.zeros(2 * F, 256, device=dev)
+    xq[:, 0] = xq[:, 128] = wq[:F, 0] = wq[F:, 128] = 1
+    sx = torch.ones(2, M, device=dev)
+    sx[0] = gates.repeat(-(-M // len(gates)))[:M]
+    sx[1] = up
+    ops = xq.to(E4), sx, wq.to(E4), torch.ones(2 * F // 128, 2, device=dev)
+    y, hq, sh = torch.empty(M, F, dtype=torch.bfloat16, device=dev), torch.empty(M, F, dtype=E4, device=dev), torch.empty(F // 128, M, device=dev)
+    h3q.h3q_linear_fp8(*ops, y, epilogue=h3q.H3Q_EPI_SWIGLU)
+    h3q.h3q_linear_fp8_swiglu_quant(*ops, hq, sh)
+    assert torch.equal(sh, sh[:1].expand_as(sh)) or torch.isnan(sh).any()
+    return sx[0], y, hq, sh[0].double() * 448
+
+
+@pytest.mark.parametrize("up", [1.0, 16.0])
+@pytest.mark.parametrize("M", [16, 48, 4096])
+def test_silu_is_accurate(h3q, cuda_device, M, up):
+    """2^x within two units of the last place (4 x 2^-24 of its value), one rounding each for what
+    lies past the first product, 1 + e, the Newton step, the last product and the scale: 9 x 2^-24.
+    (The scale is at least 2^-126, so it shows no |h| below 448 x 2^-126: 16 silu(-87.3) is above.)"""
+    assert h3q.h3q_test_fp8_plan(M, 256, 2560, h3q.H3Q_EPI_SWIGLU)[0] == {16: 16, 48: 48, 4096: 0}[M]
+    g = torch.Generator().manual_seed(M)
+    parts = [torch.rand(1500, generator=g) * 174.3 - 87.3, torch.randn(1500, generator=g) * 4,
+             torch.randn(1000, generator=g) * 2.0 ** torch.randint(-60, 4, (1000,), generator=g).float(),
+             torch.tensor([-87.3, -87.0, -64.0, -1.0, -2.0 ** -40, 2.0 ** -40, 1.0, 17.0, 88.0, 89.0, 1e4, 1e37])]
+    gates = torch.cat(parts).clamp(min=-87.3)
+    gates = gates[torch.randperm(len(gates), generator=g)].to(cuda_device)
+    for i in range(0, len(gates), M):
+        at, y, hq, got = _silu_of(h3q, gates[i : i + M], M, cuda_device, up)
+        v = at.double()
+        want = v * torch.sigmoid(v) * up
+        shown = want.abs().clamp(min=448 * 2.0 ** -126)
+        err = (got - shown).abs() / shown
+        assert err.max() <= 9 * 2.0 ** -24, (at[err.argmax()].item(), err.max().item() * 2 ** 24)
+        top = want.abs() > 448 * 2.0 ** -126
+        assert (hq.float()[top] == 448 * torch.sign(at)[top, None]).all()
+        assert ((y.double() - want[:, None]).abs() <= 2.0 ** -8 * (1 + 2.0 ** -15) * want.abs()[:, None]).all()
+
+
+@pytest.mark.parametrize("M", [16, 4096])
+def test_silu_at_its_ends(h3q, cuda_device, M):
+    """Gates under -87.3 count as 0, the largest ones as themselves, NaN as NaN."""
+    low = torch.tensor([-87.4, -88.0, -88.8, -90.0, -100.0, -104.0, -127.5, -1e3, -1e10, -1e38, -3.4e38], device=cuda_device)
+    _, y, _, got = _silu_of(h3q, low, M, cuda_device)
+    assert (got <= 2.0 ** -119).all() and (y.abs() <= 2.0 ** -119).all()
+    high = torch.tensor([88.8, 127.5, 1e3, 1e10, 1e38, 3.38e38], device=cuda_device)
+    at, y, hq, got = _silu_of(h3q, high, M, cuda_device)
+    assert torch.equal(y[:, 0], at.bfloat16()) and (hq.float() == 448).all()
+    assert ((got - at.double()).abs() <= 2.0 ** -23 * at.double()).all()
+    _, y, hq, got = _silu_of(h3q, torch.tensor([float("nan")], device=cuda_device), M, cuda_device)
+    assert torch.isnan(y).all() and torch.isnan(hq.float()).all() and torch.isnan(got).all()
+
+
 # the K axis split over two to eight CTAs, token tiles of every size, and several output
 # tiles for each SM pair with an odd number of K blocks
 LONG_SHAPES = [(1, 14336, 1024), (9, 14336, 1000), (30, 14336, 1024), (60, 14336, 1016), (100, 14336, 1024),
