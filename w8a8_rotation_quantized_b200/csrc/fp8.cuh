@@ -7,7 +7,8 @@
 //              s = 0). The bound 2^-126 keeps 1 / s finite.
 //   product    part_b = sum over the K block b of xq wq (tensor cores, fp32),
 //              acc = sum_b part_b * RN(sx[b][m] * sw[n / 128][b]), fused
-//              multiply-adds in fp32, b ascending; v = acc + bias;
+//              multiply-adds in fp32, b ascending (where the K axis is split over
+//              CTAs: within each part, then the parts' sums in order); v = acc + bias;
 //              y = bf16(v), bf16(silu(v_gate) v_up), or the latter quantized
 //              again (1 x 128) straight from fp32.
 //
@@ -320,7 +321,7 @@ constexpr uint32_t kF8RegsCtl = 32, kF8RegsPromote = 112, kF8RegsLaunch = 96;
 static_assert(128 * kF8RegsCtl + 32 * kF8Warps * kF8RegsPromote <= kF8Threads * kF8RegsLaunch, "register split");
 
 struct Fp8Params {
-  int M, N, K;              // N: output columns (SwiGLU: F)
+  int M, N;                 // N: output columns (SwiGLU: F)
   int KB;                   // K blocks: ceil(K / 128)
   int num_m, num_n, num_tiles, group_m;
   float inv_per_group, inv_group_m;  // 1 / (group_m num_n), 1 / group_m

@@ -349,7 +349,6 @@ h3q_status launch_gemm_fp8_large(const uint8_t* a, const float* sx, int64_t M, i
   h3q::Fp8Params p{};
   p.M = static_cast<int>(M);
   p.N = static_cast<int>(N_out);
-  p.K = static_cast<int>(K);
   p.KB = static_cast<int>((K + 127) / 128);
   p.num_m = static_cast<int>((M + 2 * h3q::kBM - 1) / (2 * h3q::kBM));
   p.num_n = (EPI == h3q::kF8BF16) ? static_cast<int>((N_out + h3q::kBN - 1) / h3q::kBN)
