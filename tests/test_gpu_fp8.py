@@ -536,6 +536,63 @@ def test_waits_that_run_out(h3q, cuda_device, M, K, N, epilogue, limit_ns):
     assert torch.equal(y, want)
 
 
+@pytest.mark.parametrize("M", [1, 40, 700])
+@pytest.mark.parametrize("captured", [False, True])
+def test_operands_from_another_stream(h3q, cuda_device, M, captured):
+    """A call behind a join of two streams waits for both, eager and in a graph: one operand comes from
+    the call before it in its stream, the other late from a side stream, whose call in turn follows the
+    main stream's."""
+    K, N, F, dev = 1360, 1032, 640, cuda_device
+    wq, sw = _prepare(h3q, torch.randn(N, K, generator=torch.Generator().manual_seed(1)).to(dev) * 0.02)
+    gq, sg = _prepare(h3q, torch.randn(2 * F, K, generator=torch.Generator().manual_seed(2)).to(dev) * 0.02)
+    x, late = (torch.empty(M, K, dtype=torch.bfloat16, device=dev) for _ in range(2))
+    bias = torch.empty(N, dtype=torch.bfloat16, device=dev)
+    xq, sx = _quantize(h3q, x.zero_())
+    hq, sh = torch.empty(M, F, dtype=E4, device=dev), torch.empty(F // 128, M, device=dev)
+    y, z = torch.empty(M, N, dtype=torch.bfloat16, device=dev), torch.empty(M, F, dtype=torch.bfloat16, device=dev)
+    lq, sl = torch.empty_like(xq), torch.empty_like(sx)
+    side = torch.cuda.Stream()
+
+    def step():
+        h3q.h3q_fp8_quantize(x, xq, sx)
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000)
+            late.add_(x)
+            bias.copy_(x[0, :N])
+            h3q.h3q_fp8_quantize(late, lq, sl)
+        h3q.h3q_linear_fp8_swiglu_quant(xq, sx, gq, sg, hq, sh)
+        torch.cuda.current_stream().wait_stream(side)
+        h3q.h3q_linear_fp8(lq, sl, wq, sw, y, bias=bias)
+        h3q.h3q_linear_fp8(xq, sx, gq, sg, z, epilogue=h3q.H3Q_EPI_SWIGLU)
+
+    graph = torch.cuda.CUDAGraph()
+    if captured:
+        with torch.cuda.graph(graph):
+            step()
+    for seed in range(5):
+        x.copy_(_input(M, K, seed, dev))
+        late.copy_(_input(M, K, seed + 10, dev))
+        both = late + x
+        torch.cuda.synchronize()
+        graph.replay() if captured else step()
+        torch.cuda.synchronize()
+        for t, got in ((x, (xq, sx)), (both, (lq, sl))):
+            want = _quantize(h3q, t)
+            torch.cuda.synchronize()
+            assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+        want = [torch.empty_like(t) for t in (hq, sh, y, z)]
+        h3q.h3q_linear_fp8_swiglu_quant(xq, sx, gq, sg, want[0], want[1])
+        torch.cuda.synchronize()
+        h3q.h3q_linear_fp8(lq, sl, wq, sw, want[2], bias=x[0, :N].contiguous())
+        torch.cuda.synchronize()
+        h3q.h3q_linear_fp8(xq, sx, gq, sg, want[3], epilogue=h3q.H3Q_EPI_SWIGLU)
+        torch.cuda.synchronize()
+        for t, w in zip((hq, sh, y, z), want):
+            assert torch.equal(t.view(torch.uint8), w.view(torch.uint8))
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+
+
 def _some(n):
     """Rows at both ends, and at and past element 2^31 of rows of 14336."""
     return torch.cat([torch.arange(0, 3), torch.arange(149795, 149799), torch.arange(n - 3, n)])
