@@ -362,18 +362,23 @@ __device__ __forceinline__ void f8_promote(float (&acc)[32], const uint32_t (&r)
 //   warps 18-19  MMA issue (leader CTA), one per buffer, so that each has two K blocks'
 //                time for one.
 // What bounds it: per SM and K block the MMAs take 512 cycles, reading the 128 KB of
-// partial sums 256 and their multiply-adds 256 of the fp32 pipe, in parallel. Measured 640
-// to 665 cycles a K block and some 2700 an output tile between blocks; the same kernel
+// partial sums 256 and their multiply-adds 256 of the fp32 pipe, in parallel. Measured some
+// 710 cycles a K block and 2300 an output tile between blocks (whole calls at zero operands
+// and the full clock: 14 tiles of 42 blocks a pair 232 us, 19 of 112 793); the same kernel
 // promoting once a tile (other results, for the comparison) takes 520. At random data the
-// board's power limit sets in: 4096 x 5376 x 16128 takes 226 us at the full 1.84 GHz (zero
-// operands) and 280 at the 1.5 GHz that the limit leaves, 16384 x 14336 x 5376 1.04 ms at
-// 1.36 GHz. What counted on the way (16384 x 14336 x 5376, 3.0 ms at first): arrivals at
+// board's power limit sets in as well: 4096 x 5376 x 16128 takes 232 us at the full
+// 1.965 GHz (zero operands), 289 alone with random ones and 340 back to back, at 1.4 GHz;
+// 16384 x 14336 x 5376 0.79 ms, 1.07 and 1.24, at 1.2 to 1.3 GHz. A library product with
+// one scale for the whole tensor, so without promotion, takes 186, 235 and 278 us in the
+// first case, 0.72, 0.89 and 1.03 ms in the second: the promotion's cost, 10% to 25%.
+// What counted on the way (16384 x 14336 x 5376, 3.0 ms at first): arrivals at
 // the partner CTA without a cluster-scope release (-40%); control roles run by converged
 // warps, their descriptors in uniform registers; scales fetched ahead instead of one block
-// before (-15%); no register spills (addresses of shared memory as constants); the next
-// block's scales and completion test fetched behind the release of this one (-15%). Halves
-// of a block as MMAs of 128 columns ran slower (the A tile is read twice for the same
-// work), and so did promotion by eight warps of 128 columns each.
+// before (-15%); hardly any register spills (4 bytes in the bf16 form; addresses of shared
+// memory as constants); the next block's scales and completion test fetched behind the
+// release of this one (-15%). Halves of a block as MMAs of 128 columns ran slower (the A
+// tile is read twice for the same work), and so did promotion by eight warps of 128
+// columns each.
 template <int EPI>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
     gemm_fp8_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -739,6 +744,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kF8Threads, 1)
 // loaded: the TMA would fill them with zeros, but is slow at it (one token, 5376 x 28672:
 // 34.3 us with 15 such rows a load, 28.4 without). What their place in shared memory holds
 // reaches only columns that are not written.
+// (Tiles of 64 tokens, and of 128 with SwiGLU, spill 16 bytes of registers a thread.)
 constexpr int kF8sMaxStages = 12;
 constexpr int kF8sThreads = 384;  // eight promotion warps, operands, MMA, scales, one idle until the output
 constexpr int kF8sScaleRing = 16;

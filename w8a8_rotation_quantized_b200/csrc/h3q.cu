@@ -247,9 +247,10 @@ struct Fp8Waits {
 };
 
 // Which fp8 product runs is decided by estimates of their times, fitted to measured ones
-// (330 random shapes of 49 to 1500 tokens, K to 14336, each by every kernel, in a graph; the
-// choice costs 1% over the best of them on the mean): the rounds over the SMs times the K
-// blocks of a tile times a step, the ends of the call, and what every further round adds.
+// (330 random shapes of 49 to 1500 tokens, K to 14336, each by every kernel, in a graph;
+// over these same shapes the choice costs 1% over the best of them on the mean): the rounds
+// over the SMs times the K blocks of a tile times a step, the ends of the call, and what
+// every further round adds.
 // The large kernel's tile is 256 x 256 on two SMs. Measured on both sides of the border, for
 // example (us, few tokens against large): 169 x 5216 x 3680 14.8, 20.9; 157 x 10032 x 584
 // 10.5, 36.5; 161 x 2672 x 7024 16.7, 14.6; 413 x 4240 x 12208 64.3, 36.0; SwiGLU 82 x 6896
@@ -269,7 +270,9 @@ Fp8Plan plan_gemm_fp8_small(int64_t M, int64_t N_out, int64_t KB, int sms) {
   // was seven eighths of the SMs for three and four, two thirds for six and eight (four
   // thirds at two an SM); past it a launch takes a second round (24 clusters of six: 30 us
   // instead of 18). One token, K 5376, in a graph: N 5376 split six ways 9.3 us, four
-  // 9.0, not 18.1; N 16128 two 17.4, not 19.2; SwiGLU to 14336 not 27.0, two 27.6.
+  // 9.0, not 18.1; N 16128 two 17.4, not 19.2; SwiGLU to 14336 not 27.0, two 27.6. (The
+  // rule takes the most that fits, six in the first of these. Six had been the faster,
+  // 10.4 to 11.0, until rows past the last token were no longer loaded.)
   const bool fits_two = R * TM <= 64;
   using Cfg = h3q::Fp8Small<R, TM>;
   Fp8Plan pl{TM, 1, 0, 0, Cfg::kTmem, 0.0};
