@@ -593,6 +593,38 @@ def test_operands_from_another_stream(h3q, cuda_device, M, captured):
     assert h3q.h3q_get_device_status() == h3q.H3Q_OK
 
 
+def test_every_variant_on_four_streams_at_once(h3q, cuda_device):
+    """Clusters of all kernels share the SMs, their shared and their tensor memory: each call's result
+    is the one it has alone, and no wait runs out."""
+    calls = []
+    for M, K, N, _, _ in LINEAR_VARIANTS:
+        ops = _operands(h3q, M, K, N, M + N, cuda_device, False)[:4]
+        calls.append((h3q.h3q_linear_fp8, ops, [torch.empty(M, N, dtype=torch.bfloat16, device=cuda_device)]))
+    for M, K, F, _, _ in SWIGLU_VARIANTS:
+        ops = _operands(h3q, M, K, 2 * F, M + F, cuda_device, False)[:4]
+        calls.append((h3q.h3q_linear_fp8_swiglu_quant, ops, [torch.empty(M, F, dtype=E4, device=cuda_device),
+                                                             torch.empty(F // 128, M, device=cuda_device)]))
+    want = []
+    for f, ops, out in calls:
+        f(*ops, *out)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in out])
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    got = [[[torch.empty_like(t) for t in out] for _, _, out in calls] for _ in streams]
+    torch.cuda.synchronize()
+    for turn in range(3):
+        for i in range(len(calls)):
+            for j, st in enumerate(streams):  # each stream begins elsewhere
+                at = (i + j * len(calls) // 4 + turn) % len(calls)
+                f, ops, _ = calls[at]
+                f(*ops, *got[j][at], stream=st)
+    torch.cuda.synchronize()
+    assert h3q.h3q_get_device_status() == h3q.H3Q_OK
+    for outs in got:
+        for a, b in zip(outs, want):
+            assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(a, b))
+
+
 def _some(n):
     """Rows at both ends, and at and past element 2^31 of rows of 14336."""
     return torch.cat([torch.arange(0, 3), torch.arange(149795, 149799), torch.arange(n - 3, n)])
