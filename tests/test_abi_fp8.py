@@ -128,6 +128,10 @@ def test_plan_rejects():
         args[i] = bad
         assert h3q.lib.h3q_test_fp8_plan(*args) == INV, (i, bad)
     assert h3q.lib.h3q_test_fp8_plan(4, 512, 384, h3q.H3Q_EPI_SWIGLU, 148, plan) == INV
+    for i, bad in [(0, 2**31), (1, 2**40), (2, 2**60)]:
+        args = list(ok)
+        args[i] = bad
+        assert h3q.lib.h3q_test_fp8_plan(*args) == UNS, (i, bad)
     assert h3q.lib.h3q_test_fp8_plan(*ok) == OK
 
 

@@ -807,6 +807,7 @@ h3q_status h3q_test_stalled_linear_fp8(const uint8_t* xq, const float* sx, int64
 h3q_status h3q_test_fp8_plan(int64_t M, int64_t K, int64_t N, int epilogue, int sms, int32_t* plan) {
   if (M < 1 || !valid_fp8_k(K) || N <= 0 || N % 8 != 0 || sms < 2 || !plan) return H3Q_ERR_INVALID_ARG;
   if (epilogue != H3Q_EPI_NONE && (epilogue != H3Q_EPI_SWIGLU || N % 256 != 0)) return H3Q_ERR_INVALID_ARG;
+  if (M > INT32_MAX - 256 || N > INT32_MAX - 512 || K > INT32_MAX - 256) return H3Q_ERR_UNSUPPORTED;
   const Fp8Plan p = epilogue == H3Q_EPI_SWIGLU ? plan_gemm_fp8<2>(M, K, N / 2, sms) : plan_gemm_fp8<1>(M, K, N, sms);
   plan[0] = p.tile;
   plan[1] = p.splits;
